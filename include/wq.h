@@ -53,6 +53,11 @@
  *    bscale  uint8 [N, K/16]   FP8 E4M3 block scale, one per 16 consecutive k
  *    global_scale float [1]    per-tensor fp32 scale g
  *    w_hat = e2m1(code) * e4m3(bscale) * g
+ * Packed MXFP4 format (the OCP "Microscaling Formats (MX)" specification, v1.0:
+ * E2M1 elements, one E8M0 scale per block of 32; the pages have no counterpart):
+ *    codes   uint8 [N, K/2]    nibbles as NVFP4
+ *    bscale  uint8 [N, K/32]   E8M0 block scale: 2^(byte - 127), 255 = NaN
+ *    w_hat = e2m1(code) * 2^(bscale - 127), exact in bf16
  */
 #ifndef WQ_H_
 #define WQ_H_
@@ -73,7 +78,7 @@ typedef enum {
 } wq_status;
 
 /* Linear formats for wq_linear_workspace_size. */
-enum { WQ_FMT_INT4 = 0, WQ_FMT_NVFP4 = 1 };
+enum { WQ_FMT_INT4 = 0, WQ_FMT_NVFP4 = 1, WQ_FMT_MXFP4 = 2 };
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* wq_status_string(int status);
@@ -86,10 +91,12 @@ const char* wq_last_error(void);
 int wq_int4_sizes(int64_t N, int64_t K, int group_size, size_t* qweight_bytes,
                   size_t* scales_bytes, size_t* zeros_bytes);
 int wq_nvfp4_sizes(int64_t N, int64_t K, size_t* codes_bytes, size_t* bscale_bytes);
+int wq_mxfp4_sizes(int64_t N, int64_t K, size_t* codes_bytes, size_t* bscale_bytes);
 
-/* Scratch bytes wq_linear_int4 / wq_linear_nvfp4 use for an [M, K] x [N, K]
- * problem (format WQ_FMT_*, act_fp4 as in wq_linear_nvfp4).  W4A4 requires a
- * workspace of this size.  W4A16 never requires one: a non-zero size means a
+/* Scratch bytes wq_linear_int4 / wq_linear_nvfp4 / wq_linear_mxfp4 use for an
+ * [M, K] x [N, K] problem (format WQ_FMT_*, act_fp4 as in wq_linear_nvfp4).
+ * W4A4 requires a workspace of this size.  W4A16 never requires one (MXFP4
+ * uses none); for INT4 and NVFP4 a non-zero size means a
  * prefill GEMM with few output tiles (under half the SMs) that, given a
  * workspace of at least this size, splits K over several CTAs per tile (fp32
  * partial tiles, then a reduction launch that sums them in split order, so the
@@ -136,6 +143,29 @@ int wq_quantize_int4(const uint16_t* W, int64_t N, int64_t K, int bits, int grou
  * block scale is 0.  Bit-for-bit deterministic. */
 int wq_quantize_nvfp4(const uint16_t* W, int64_t N, int64_t K, const float* scale_s,
                       uint8_t* codes, uint8_t* bscale, float* global_scale, void* stream);
+
+/* wq_quantize_mxfp4 -- MXFP4 pack (OCP MX specification v1.0, section 6.3:
+ * the shared exponent is the exponent of the block's largest magnitude less
+ * that of E2M1's largest value).
+ *   W        bf16 [N, K]
+ *   scale_s  fp32 [K] or NULL, as for INT4
+ *   codes, bscale: outputs in the packed MXFP4 format above.
+ * Per block of 32 along k, w' = W or W * scale_s (fp32 multiply):
+ *   e = clamp(floor(log2 max|w'|) - 2, -127, 127), -127 for an all-zero block;
+ *   bscale = e + 127; code = nearest E2M1 of w' / 2^e (exact), ties to the even
+ *   code, saturating at 6, sign bit = sign of w'.
+ * A block that holds an infinity or a NaN gets the scale 255 (NaN) and zero
+ * codes, so that its products are NaN.  Rows are packed independently: the
+ * pack of a stack [E, N, K] is the pack of [E * N, K].  Bit-for-bit
+ * deterministic. */
+int wq_quantize_mxfp4(const uint16_t* W, int64_t N, int64_t K, const float* scale_s, uint8_t* codes,
+                      uint8_t* bscale, void* stream);
+
+/* wq_dequantize_mxfp4 -- the values an MXFP4 pack stands for, W bf16 [N, K]
+ * (exact; NaN under a NaN scale, and an infinity where 6 * 2^126 or more is
+ * stored, which wq_quantize_mxfp4 never does). */
+int wq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* bscale, int64_t N, int64_t K, uint16_t* W,
+                        void* stream);
 
 /* wq_gptq_int4 -- GPTQ INT4 quantize-and-pack with second-order error
  * feedback ("quantization primer" section 6 "GPTQ": quantize a weight,
@@ -298,20 +328,59 @@ int wq_linear_nvfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
                     const uint8_t* bscale, const float* global_scale, int act_fp4,
                     const float* act_inv_s, uint16_t* Y, void* ws, size_t ws_bytes, void* stream);
 
-/* One quantized Linear of a group (W4A16; see wq_linear_int4 / wq_linear_nvfp4
- * for the meaning of each field).  `format` is WQ_FMT_INT4 or WQ_FMT_NVFP4;
- * fields of the other format are ignored. */
+/* wq_linear_mxfp4 -- Y = (X * act_inv_s) * dequant(Wq)^T for an MXFP4 pack.
+ *   act_fp4 = 0: W4A16, activations stay bf16 (needs no workspace).
+ *   act_fp4 = 1: W4A4: X * act_inv_s is first quantized to MXFP4 along K (the
+ *            wq_quantize_mxfp4 rule applied to X), and the product runs on the
+ *            block-scaled FP4 tensor cores; K % 64 == 0; needs workspace.
+ *   other arguments as for wq_linear_int4. */
+int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint8_t* codes,
+                    const uint8_t* bscale, int act_fp4, const float* act_inv_s, uint16_t* Y, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* The 4-bit weights of E experts [N, K] each, one pack after the other. */
+typedef struct {
+  int format;                 /* WQ_FMT_INT4, WQ_FMT_NVFP4 or WQ_FMT_MXFP4 */
+  int64_t E, N, K;            /* 1 <= E <= 1024, E * N < 2^31 */
+  const void* packed;         /* INT4 qweight uint32 [E, N, K/8]; NVFP4 / MXFP4 codes uint8 [E, N, K/2] */
+  const uint16_t* scales;     /* INT4 fp16 [E, N, K/G] */
+  const uint32_t* zeros;      /* INT4 uint32 [E, N, ceil(K/G/8)], NULL for symmetric packs */
+  int group_size;             /* INT4: 32, 64 or 128 */
+  int zero_point;             /* INT4: 1 asymmetric, 0 symmetric */
+  const uint8_t* bscale;      /* NVFP4 E4M3 [E, N, K/16]; MXFP4 E8M0 [E, N, K/32] */
+  const float* global_scale;  /* NVFP4 fp32 [E], one tensor scale per expert, 4-byte aligned */
+} wq_expert_stack;
+
+/* wq_linear_experts -- the quantized Linear of a mixture of experts: rows of X
+ * sorted by expert, ragged sizes ("Lance-Quant", section "校准阶段", quantizes
+ * the expert siblings of each projection; the pages give no runtime for them).
+ *   Y[i] = X[i] * dequant(W_e)^T  for offsets[e] <= i < offsets[e + 1]
+ *   X        bf16 [T, K]
+ *   offsets  int32 [E + 1], DEVICE memory (read by the kernel: the host needs
+ *            no copy of it), 4-byte aligned, not decreasing, within [0, T]
+ *   Y        bf16 [T, N]; rows before offsets[0] and from offsets[E] on are
+ *            left as they were
+ * W4A16, fp32 accumulation, no workspace.  An expert may hold no row or all of
+ * them; T = 0 computes nothing (X, Y and offsets may then be NULL).  Offsets
+ * that decrease or leave [0, T] make the call compute nothing, and the next
+ * wq_device_error returns WQ_ERR_ARG. */
+int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, const int32_t* offsets,
+                      uint16_t* Y, void* stream);
+
+/* One quantized Linear of a group (W4A16; see wq_linear_int4 / wq_linear_nvfp4 /
+ * wq_linear_mxfp4 for the meaning of each field).  `format` is WQ_FMT_INT4,
+ * WQ_FMT_NVFP4 or WQ_FMT_MXFP4; fields of the other formats are ignored. */
 typedef struct {
   int format;
   int64_t N, K;
   const uint16_t* X;          /* bf16 [M, K] */
   const float* act_inv_s;     /* fp32 [K] or NULL */
-  const void* packed;         /* INT4 qweight (uint32 [N, K/8]) or NVFP4 codes (uint8 [N, K/2]) */
+  const void* packed;         /* INT4 qweight (uint32 [N, K/8]) or NVFP4 / MXFP4 codes (uint8 [N, K/2]) */
   const uint16_t* scales;     /* INT4 fp16 [N, K/G] */
   const uint32_t* zeros;      /* INT4 packed zero points, NULL for a symmetric pack */
   int group_size;             /* INT4: 32, 64 or 128 (32 runs the CUDA-core GEMV) */
   int zero_point;             /* INT4: 1 asymmetric, 0 symmetric */
-  const uint8_t* bscale;      /* NVFP4 E4M3 [N, K/16] */
+  const uint8_t* bscale;      /* NVFP4 E4M3 [N, K/16], MXFP4 E8M0 [N, K/32] */
   const float* global_scale;  /* NVFP4 fp32 [1] */
   uint16_t* Y;                /* bf16 [M, N] */
 } wq_linear_item;
@@ -326,7 +395,7 @@ typedef struct {
  * or 128 or NVFP4, 16-byte aligned X / packed / act_inv_s, 4-byte aligned
  * scale data) run as one launch for all their weight kinds together, up to 24
  * items and 8 distinct activation vectors; the other items (M > 2, group 32,
- * other K) run one by one after them.  Items must not alias each other's
+ * other K, MXFP4) run one by one after them.  Items must not alias each other's
  * outputs.  Needs no workspace.
  * Returns the first failing item's status. */
 int wq_linear_group(const wq_linear_item* items, int count, int64_t M, void* stream);
@@ -365,7 +434,8 @@ int wq_selftest_timeout(int* waited_ok, void* stream);
  * current GPU.  WQ_OK if no kernel reported a problem since the last call,
  * WQ_ERR_TIMEOUT if a bounded wait inside a kernel gave up (the kernel then
  * exited early and its outputs are undefined), WQ_ERR_ARG if
- * wq_gptq_hessian_factor met a Hessian that is not positive definite,
+ * wq_gptq_hessian_factor met a Hessian that is not positive definite or
+ * wq_linear_experts offsets that decrease or leave [0, T],
  * WQ_ERR_CUDA if the stream itself failed. */
 int wq_device_error(void* stream);
 

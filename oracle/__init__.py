@@ -67,6 +67,12 @@ def _L():
         lib.oracle_quantize_nvfp4.argtypes = [P, I64, I64, P, P, P, P]
         lib.oracle_dequant_nvfp4.restype = None
         lib.oracle_dequant_nvfp4.argtypes = [P, P, ctypes.c_float, I64, I64, P, I64, P]
+        lib.oracle_e8m0_decode.restype = ctypes.c_double
+        lib.oracle_e8m0_decode.argtypes = [ctypes.c_uint8]
+        lib.oracle_quantize_mxfp4.restype = I
+        lib.oracle_quantize_mxfp4.argtypes = [P, I64, I64, P, P, P]
+        lib.oracle_dequant_mxfp4.restype = None
+        lib.oracle_dequant_mxfp4.argtypes = [P, P, I64, I64, P]
         lib.oracle_activations_f64.restype = None
         lib.oracle_activations_f64.argtypes = [P, I64, I64, P, P]
         lib.oracle_matmul_abT.restype = None
@@ -196,6 +202,28 @@ def dequant_nvfp4(p: dict, rows=None) -> np.ndarray:
     _L().oracle_dequant_nvfp4(_ptr(np.ascontiguousarray(p["codes"], dtype=np.uint8)),
                               _ptr(np.ascontiguousarray(p["bscale"], dtype=np.uint8)),
                               float(p["g"]), R, C, _ptr(r), nr, _ptr(out))
+    return out
+
+
+def e8m0_decode(code) -> float:
+    return _L().oracle_e8m0_decode(int(code))
+
+
+def quantize_mxfp4(A, s=None) -> dict:
+    a = as_bits16(A)
+    R, C = a.shape
+    codes = np.zeros((R, C // 2), dtype=np.uint8)
+    bscale = np.zeros((R, C // 32), dtype=np.uint8)
+    if _L().oracle_quantize_mxfp4(_ptr(a), R, C, _ptr(_f32(s)), _ptr(codes), _ptr(bscale)) != 0:
+        raise ValueError("oracle_quantize_mxfp4: invalid arguments")
+    return dict(codes=codes, bscale=bscale, N=R, K=C)
+
+
+def dequant_mxfp4(p: dict) -> np.ndarray:
+    R, C = p["N"], p["K"]
+    out = np.empty((R, C), dtype=np.float64)
+    _L().oracle_dequant_mxfp4(_ptr(np.ascontiguousarray(p["codes"], dtype=np.uint8)),
+                              _ptr(np.ascontiguousarray(p["bscale"], dtype=np.uint8)), R, C, _ptr(out))
     return out
 
 

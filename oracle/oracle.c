@@ -320,6 +320,64 @@ void oracle_dequant_nvfp4(const uint8_t* codes, const uint8_t* bscale, float g, 
 }
 
 /* ------------------------------------------------------------------ */
+/* MXFP4 (OCP MX specification v1.0): E2M1 elements, one E8M0 per 32   */
+/* ------------------------------------------------------------------ */
+
+double oracle_e8m0_decode(uint8_t b) { return b == 255 ? NAN : ldexp(1.0, (int)b - 127); }
+
+/* MXFP4 quantize of A [R, C] (times s per column, one fp32 multiply).  Per 32
+ * consecutive elements of a row, from the largest magnitude m:
+ *   e = clamp(floor(log2 m) - 2, -127, 127), -127 when m = 0; byte e + 127;
+ *   code = E2M1(A' / 2^e) (the quotient is exact in fp64).
+ * A block with an infinity or a NaN: byte 255, codes 0. */
+int oracle_quantize_mxfp4(const uint16_t* A, int64_t R, int64_t C, const float* s, uint8_t* codes,
+                          uint8_t* bscale) {
+  if (R <= 0 || C <= 0 || C % 32) return ORACLE_ERR_ARG;
+  memset(codes, 0, (size_t)(R * C / 2));
+#pragma omp parallel for schedule(static)
+  for (int64_t r = 0; r < R; ++r) {
+    for (int64_t b = 0; b < C / 32; ++b) {
+      float m = 0.0f;
+      int bad = 0;
+      for (int64_t c = b * 32; c < b * 32 + 32; ++c) {
+        float a = fabsf(wprime(A, s, C, r, c));
+        if (!isfinite(a)) bad = 1;
+        if (a > m) m = a;
+      }
+      if (bad) {
+        bscale[r * (C / 32) + b] = 255;
+        continue;
+      }
+      int e = -127;
+      if (m > 0.0f) {
+        int p;
+        frexp((double)m, &p); /* m = f 2^p, f in [0.5, 1): floor(log2 m) = p - 1 */
+        e = p - 3;
+        if (e < -127) e = -127;
+        if (e > 127) e = 127;
+      }
+      bscale[r * (C / 32) + b] = (uint8_t)(e + 127);
+      for (int64_t c = b * 32; c < b * 32 + 32; ++c) {
+        /* rounding the quotient to fp32 only touches values below 2^-126, which encode 0 either way */
+        uint8_t code = oracle_e2m1_encode((float)ldexp((double)wprime(A, s, C, r, c), -e));
+        codes[r * (C / 2) + c / 2] |= (uint8_t)(code << (4 * (c % 2)));
+      }
+    }
+  }
+  return ORACLE_OK;
+}
+
+/* MXFP4 dequantize: e2m1(code) * 2^e in fp64. */
+void oracle_dequant_mxfp4(const uint8_t* codes, const uint8_t* bscale, int64_t R, int64_t C, double* out) {
+#pragma omp parallel for schedule(static)
+  for (int64_t r = 0; r < R; ++r)
+    for (int64_t c = 0; c < C; ++c) {
+      uint8_t code = (codes[r * (C / 2) + c / 2] >> (4 * (c % 2))) & 0xF;
+      out[r * C + c] = oracle_e2m1_decode(code) * oracle_e8m0_decode(bscale[r * (C / 32) + c / 32]);
+    }
+}
+
+/* ------------------------------------------------------------------ */
 /* Linear ([P4] section 4 "W4A16": weights 4-bit, activations 16-bit)   */
 /* ------------------------------------------------------------------ */
 

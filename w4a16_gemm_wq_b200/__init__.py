@@ -1,4 +1,4 @@
-"""B200-native group-wise 4-bit weight-only quantization (INT4 / NVFP4) and the
+"""B200-native group-wise 4-bit weight-only quantization (INT4 / NVFP4 / MXFP4) and the
 quantized Linear Y = X * dequant(Wq)^T.
 
 This module is a thin ctypes binding over ``libwq.so`` (C ABI in
@@ -10,7 +10,7 @@ loaded every call raises.
 Functions carry the C names:
     wq_quantize_int4, wq_gptq_hessian_factor, wq_gptq_int4, wq_quantize_nvfp4, awq_search_scale,
     awq_search_scale_shared, wq_quantize_layers, wq_linear_int4, wq_linear_nvfp4, wq_linear_group,
-    wq_device_error
+    wq_quantize_mxfp4, wq_dequantize_mxfp4, wq_linear_mxfp4, wq_linear_experts, wq_device_error
 """
 from __future__ import annotations
 
@@ -24,7 +24,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libwq.so")
 
 WQ_OK, WQ_ERR_ARG, WQ_ERR_CUDA, WQ_ERR_UNSUPPORTED, WQ_ERR_TIMEOUT = range(5)
-WQ_FMT_INT4, WQ_FMT_NVFP4 = 0, 1
+WQ_FMT_INT4, WQ_FMT_NVFP4, WQ_FMT_MXFP4 = 0, 1, 2
 
 # (name, restype, argtypes) of every symbol declared in include/wq.h
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -34,6 +34,11 @@ SIGNATURES = {
     "wq_last_error": (ctypes.c_char_p, []),
     "wq_int4_sizes": (_I, [_I64, _I64, _I, _PSZ, _PSZ, _PSZ]),
     "wq_nvfp4_sizes": (_I, [_I64, _I64, _PSZ, _PSZ]),
+    "wq_mxfp4_sizes": (_I, [_I64, _I64, _PSZ, _PSZ]),
+    "wq_quantize_mxfp4": (_I, [_P, _I64, _I64, _P, _P, _P, _P]),
+    "wq_dequantize_mxfp4": (_I, [_P, _P, _I64, _I64, _P, _P]),
+    "wq_linear_mxfp4": (_I, [_P, _I64, _I64, _I64, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "wq_linear_experts": (_I, [_P, _P, _I64, _P, _P, _P]),
     "wq_linear_workspace_size": (_I, [_I64, _I64, _I64, _I, _I, _PSZ]),
     "awq_search_workspace_size": (_I, [_I64, _I64, _I64, _I, _I, _PSZ]),
     "wq_quantize_int4": (_I, [_P, _I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P]),
@@ -139,6 +144,40 @@ class PackedNVFP4:
         return self.codes.numel() + self.bscale.numel() + 4
 
 
+@dataclasses.dataclass
+class PackedMXFP4:
+    codes: torch.Tensor   # uint8 [N, K/2]
+    bscale: torch.Tensor  # uint8 [N, K/32] (E8M0: 2^(byte - 127))
+    N: int
+    K: int
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.bscale.numel()
+
+
+@dataclasses.dataclass
+class PackedExperts:
+    """The packs of E experts' weights [N, K], one after the other (wq_expert_stack)."""
+    fmt: str                             # "int4", "nvfp4" or "mxfp4"
+    E: int
+    N: int
+    K: int
+    packed: torch.Tensor                 # INT4 qweight int32 [E, N, K/8]; else codes uint8 [E, N, K/2]
+    scales: torch.Tensor | None = None   # INT4 fp16 [E, N, K/G]
+    zeros: torch.Tensor | None = None    # INT4 int32 [E, N, ceil(K/G/8)], None for symmetric packs
+    group_size: int = 0                  # INT4
+    zero_point: int = 1                  # INT4
+    bscale: torch.Tensor | None = None   # uint8 [E, N, K/16] (NVFP4, E4M3) or [E, N, K/32] (MXFP4, E8M0)
+    global_scale: torch.Tensor | None = None  # NVFP4 fp32 [E]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size()
+                   for t in (self.packed, self.scales, self.zeros, self.bscale, self.global_scale) if t is not None)
+
+
+_PACKED = (PackedInt4, PackedNVFP4, PackedMXFP4, PackedExperts)
+
+
 def int4_sizes(N: int, K: int, group_size: int):
     q, s, z = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().wq_int4_sizes(N, K, group_size, ctypes.byref(q), ctypes.byref(s), ctypes.byref(z)), "wq_int4_sizes")
@@ -148,6 +187,12 @@ def int4_sizes(N: int, K: int, group_size: int):
 def nvfp4_sizes(N: int, K: int):
     c, b = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load().wq_nvfp4_sizes(N, K, ctypes.byref(c), ctypes.byref(b)), "wq_nvfp4_sizes")
+    return c.value, b.value
+
+
+def mxfp4_sizes(N: int, K: int):
+    c, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().wq_mxfp4_sizes(N, K, ctypes.byref(c), ctypes.byref(b)), "wq_mxfp4_sizes")
     return c.value, b.value
 
 
@@ -166,7 +211,7 @@ def _workspace(nbytes: int, device) -> torch.Tensor | None:
 # ---------------------------------------------------------------- stage 1
 def wq_quantize_int4(W: torch.Tensor, group_size: int = 64, zero_point: int = 1, scale_s=None,
                      bits: int = 4) -> PackedInt4:
-    if isinstance(W, (PackedInt4, PackedNVFP4)):
+    if isinstance(W, _PACKED):
         raise ValueError("the layer is already quantized")  # "llm-quantize": refuse re-quantizing
     _dev(W, "W", torch.bfloat16)
     N, K = W.shape
@@ -185,7 +230,7 @@ def wq_gptq_int4(W: torch.Tensor, U: torch.Tensor, group_size: int = 128, zero_p
     """GPTQ INT4 pack of W with the inverse-Hessian factor U (fp32 [K, K] upper
     Cholesky factor of the damped inverse Hessian; see wq_gptq_hessian_factor).
     Same packed format as wq_quantize_int4."""
-    if isinstance(W, (PackedInt4, PackedNVFP4)):
+    if isinstance(W, _PACKED):
         raise ValueError("the layer is already quantized")
     _dev(W, "W", torch.bfloat16)
     N, K = W.shape
@@ -228,7 +273,7 @@ def wq_gptq_hessian_factor(X: torch.Tensor, damp: float = 0.01, out: torch.Tenso
 
 
 def wq_quantize_nvfp4(W: torch.Tensor, scale_s=None) -> PackedNVFP4:
-    if isinstance(W, (PackedInt4, PackedNVFP4)):
+    if isinstance(W, _PACKED):
         raise ValueError("the layer is already quantized")
     _dev(W, "W", torch.bfloat16)
     N, K = W.shape
@@ -240,6 +285,80 @@ def wq_quantize_nvfp4(W: torch.Tensor, scale_s=None) -> PackedNVFP4:
     _check(lib.wq_quantize_nvfp4(_ptr(W), N, K, _ptr(s), _ptr(codes), _ptr(bscale), _ptr(g), _stream()),
            "wq_quantize_nvfp4")
     return PackedNVFP4(codes, bscale, g, N, K)
+
+
+def _same_device(t0: torch.Tensor, *ts):
+    for t in ts:
+        if t is not None and t.device != t0.device:
+            raise ValueError(f"tensors on {t0.device} and {t.device}: all must be on one device")
+
+
+def wq_quantize_mxfp4(W: torch.Tensor, scale_s=None) -> PackedMXFP4:
+    """MXFP4 pack of W (bf16 [N, K]), or of W * scale_s: E2M1 codes and one power-of-two
+    scale per 32 consecutive k."""
+    if isinstance(W, _PACKED):
+        raise ValueError("the layer is already quantized")
+    _dev(W, "W", torch.bfloat16)
+    if W.dim() != 2:
+        raise ValueError("W must be [N, K]")
+    N, K = W.shape
+    s = _opt_f32(scale_s, "scale_s", K)
+    _same_device(W, s)
+    with torch.cuda.device(W.device):
+        codes = torch.empty((N, max(K // 2, 1)), dtype=torch.uint8, device=W.device)
+        bscale = torch.empty((N, max(K // 32, 1)), dtype=torch.uint8, device=W.device)
+        _check(load().wq_quantize_mxfp4(_ptr(W), N, K, _ptr(s), _ptr(codes), _ptr(bscale), _stream()),
+               "wq_quantize_mxfp4")
+    return PackedMXFP4(codes, bscale, N, K)
+
+
+def _mx_pack(p: PackedMXFP4):
+    if not isinstance(p, PackedMXFP4):
+        raise ValueError("need a PackedMXFP4")
+    _dev(p.codes, "codes", torch.uint8, (p.N, p.K // 2))
+    _dev(p.bscale, "bscale", torch.uint8, (p.N, p.K // 32))
+    return p
+
+
+def wq_dequantize_mxfp4(p: PackedMXFP4, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of an MXFP4 pack, bf16 [N, K] (exact)."""
+    _mx_pack(p)
+    dev = p.codes.device
+    W = out if out is not None else torch.empty((p.N, p.K), dtype=torch.bfloat16, device=dev)
+    _dev(W, "out", torch.bfloat16, (p.N, p.K))
+    _same_device(p.codes, p.bscale, W)
+    with torch.cuda.device(dev):
+        _check(load().wq_dequantize_mxfp4(_ptr(p.codes), _ptr(p.bscale), p.N, p.K, _ptr(W), _stream()),
+               "wq_dequantize_mxfp4")
+    return W
+
+
+def wq_quantize_experts(W: torch.Tensor, fmt: str = "mxfp4", group_size: int = 64, zero_point: int = 1) -> PackedExperts:
+    """Pack the weights of E experts (bf16 [E, N, K]) for wq_linear_experts.  Each expert's
+    pack is what the single entry point gives for its matrix; NVFP4 has one tensor scale
+    per expert."""
+    if isinstance(W, _PACKED):
+        raise ValueError("the layer is already quantized")
+    _dev(W, "W", torch.bfloat16)
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, K = W.shape
+    if E < 1:
+        raise ValueError("need at least one expert")
+    if fmt == "mxfp4":
+        p = wq_quantize_mxfp4(W.view(E * N, K))
+        return PackedExperts(fmt, E, N, K, p.codes.view(E, N, -1), bscale=p.bscale.view(E, N, -1))
+    if fmt == "int4":
+        p = wq_quantize_int4(W.view(E * N, K), group_size, zero_point)
+        return PackedExperts(fmt, E, N, K, p.qweight.view(E, N, -1), scales=p.scales.view(E, N, -1),
+                             zeros=None if p.zeros is None else p.zeros.view(E, N, -1), group_size=group_size,
+                             zero_point=zero_point)
+    if fmt == "nvfp4":
+        ps = [wq_quantize_nvfp4(W[e]) for e in range(E)]
+        return PackedExperts(fmt, E, N, K, torch.stack([p.codes for p in ps]),
+                             bscale=torch.stack([p.bscale for p in ps]),
+                             global_scale=torch.cat([p.global_scale for p in ps]))
+    raise ValueError(f"unknown format {fmt!r}: int4, nvfp4 or mxfp4")
 
 
 def awq_search_scale(W: torch.Tensor, alphas: torch.Tensor, group_size: int = 64, X: torch.Tensor | None = None,
@@ -336,7 +455,7 @@ def make_layer_items(Ws: list, act_means: list, n_alpha: int, group_size: int = 
     arr = (LayerItem * len(Ws))()
     outs = []
     for i, (W, am) in enumerate(zip(Ws, act_means)):
-        if isinstance(W, (PackedInt4, PackedNVFP4)):
+        if isinstance(W, _PACKED):
             raise ValueError("the layer is already quantized")
         _dev(W, f"Ws[{i}]", torch.bfloat16)
         N, K = W.shape
@@ -448,6 +567,87 @@ def wq_linear_nvfp4_w4a4_noalloc(X: torch.Tensor, p: PackedNVFP4, act_inv_s=None
     return Y
 
 
+def wq_linear_mxfp4(X: torch.Tensor, p: PackedMXFP4, act_fp4: int = 0, act_inv_s=None,
+                    out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = (X * act_inv_s) * dequant(p)^T; act_fp4 = 1 also packs the activations to MXFP4."""
+    _mx_pack(p)
+    _dev(X, "X", torch.bfloat16)
+    if X.dim() != 2 or X.shape[1] != p.K:
+        raise ValueError(f"X must be [M, {p.K}], got {tuple(X.shape)}")
+    M, K = X.shape
+    Y = out if out is not None else torch.empty((M, p.N), dtype=torch.bfloat16, device=X.device)
+    _dev(Y, "out", torch.bfloat16, (M, p.N))
+    s = _opt_f32(act_inv_s, "act_inv_s", K)
+    _same_device(X, p.codes, p.bscale, Y, s, ws)
+    with torch.cuda.device(X.device):
+        if ws is None:
+            ws = _workspace(linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4), X.device)
+        _check(load().wq_linear_mxfp4(_ptr(X), M, p.N, K, _ptr(p.codes), _ptr(p.bscale), act_fp4, _ptr(s), _ptr(Y),
+                                      _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream()),
+               "wq_linear_mxfp4")
+    return Y
+
+
+class ExpertStack(ctypes.Structure):
+    """Mirror of wq_expert_stack (include/wq.h)."""
+
+    _fields_ = [("format", ctypes.c_int), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("group_size", ctypes.c_int), ("zero_point", ctypes.c_int), ("bscale", ctypes.c_void_p),
+                ("global_scale", ctypes.c_void_p)]
+
+
+def _expert_stack(p: PackedExperts) -> ExpertStack:
+    """The wq_expert_stack of a pack, its tensors checked."""
+    if not isinstance(p, PackedExperts):
+        raise ValueError("need a PackedExperts")
+    E, N, K = p.E, p.N, p.K
+    w = ExpertStack(E=E, N=N, K=K)
+    if p.fmt == "int4":
+        _dev(p.packed, "packed", torch.int32, (E, N, K // 8))
+        ng = K // p.group_size if p.group_size in (32, 64, 128) else 1
+        _dev(p.scales, "scales", torch.float16, (E, N, ng))
+        if p.zero_point:
+            _dev(p.zeros, "zeros", torch.int32, (E, N, (ng + 7) // 8))
+            w.zeros = p.zeros.data_ptr()
+        w.format, w.scales, w.group_size, w.zero_point = WQ_FMT_INT4, p.scales.data_ptr(), p.group_size, p.zero_point
+        _same_device(p.packed, p.scales, p.zeros)
+    elif p.fmt in ("nvfp4", "mxfp4"):
+        block = 16 if p.fmt == "nvfp4" else 32
+        _dev(p.packed, "packed", torch.uint8, (E, N, K // 2))
+        _dev(p.bscale, "bscale", torch.uint8, (E, N, K // block))
+        w.format, w.bscale = WQ_FMT_MXFP4, p.bscale.data_ptr()
+        if p.fmt == "nvfp4":
+            _dev(p.global_scale, "global_scale", torch.float32, (E,))
+            w.format, w.global_scale = WQ_FMT_NVFP4, p.global_scale.data_ptr()
+        _same_device(p.packed, p.bscale, p.global_scale)
+    else:
+        raise ValueError(f"unknown format {p.fmt!r}: int4, nvfp4 or mxfp4")
+    w.packed = p.packed.data_ptr()
+    return w
+
+
+def wq_linear_experts(X: torch.Tensor, offsets: torch.Tensor, p: PackedExperts,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y[i] = X[i] * dequant(W_e)^T for offsets[e] <= i < offsets[e + 1]: the ragged products of a
+    mixture of experts, rows of X (bf16 [T, K]) sorted by expert, offsets int32 [E + 1] on the
+    device.  Rows outside [offsets[0], offsets[E]) are left as they are in `out`, and are zero
+    in a new result."""
+    w = _expert_stack(p)
+    _dev(X, "X", torch.bfloat16)
+    if X.dim() != 2 or X.shape[1] != p.K:
+        raise ValueError(f"X must be [T, {p.K}], got {tuple(X.shape)}")
+    T = X.shape[0]
+    _dev(offsets, "offsets", torch.int32, (p.E + 1,))
+    Y = out if out is not None else torch.zeros((T, p.N), dtype=torch.bfloat16, device=X.device)
+    _dev(Y, "out", torch.bfloat16, (T, p.N))
+    _same_device(X, offsets, p.packed, Y)
+    with torch.cuda.device(X.device):
+        _check(load().wq_linear_experts(ctypes.byref(w), _ptr(X), T, _ptr(offsets), _ptr(Y), _stream()),
+               "wq_linear_experts")
+    return Y
+
+
 class LinearItem(ctypes.Structure):
     """Mirror of wq_linear_item (include/wq.h)."""
 
@@ -479,6 +679,8 @@ def make_group(calls):
             it.format, it.packed, it.scales = WQ_FMT_INT4, p.qweight.data_ptr(), p.scales.data_ptr()
             it.zeros = None if p.zeros is None else p.zeros.data_ptr()
             it.group_size, it.zero_point = p.group_size, p.zero_point
+        elif isinstance(p, PackedMXFP4):
+            it.format, it.packed, it.bscale = WQ_FMT_MXFP4, p.codes.data_ptr(), p.bscale.data_ptr()
         else:
             it.format, it.packed = WQ_FMT_NVFP4, p.codes.data_ptr()
             it.bscale, it.global_scale = p.bscale.data_ptr(), p.global_scale.data_ptr()

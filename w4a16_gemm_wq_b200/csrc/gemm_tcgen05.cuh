@@ -83,7 +83,7 @@ struct GemmArgs {
 };
 
 // B operand modes of gemm_tcgen05_kernel.
-enum { GEMM_INT4 = 0, GEMM_NVFP4 = 1, GEMM_BF16_SQ = 2 };
+enum { GEMM_INT4 = 0, GEMM_NVFP4 = 1, GEMM_BF16_SQ = 2, GEMM_MXFP4 = 3 };
 
 // ------------------------------------------------------------------ tcgen05 helpers
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {

@@ -10,10 +10,12 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "wq.h"
 #include "awq.cuh"
+#include "experts.cuh"
 #include "gemm_fp4.cuh"
 #include "gemm_tcgen05.cuh"
 #include "gemv.cuh"
@@ -21,6 +23,7 @@
 #include "gemv_tc.cuh"
 #include "gptq.cuh"
 #include "gptq_factor.cuh"
+#include "mxfp4.cuh"
 #include "quant.cuh"
 #include "wq_common.cuh"
 
@@ -520,6 +523,71 @@ int launch_fp4_bn(wq::Fp4Args& a, const uint8_t* xcodes, const uint8_t* wcodes, 
   return cuda_check(cudaLaunchKernelEx(&cfg, wq::gemm_fp4_kernel<BN>, a), "fp4 gemm launch");
 }
 
+// ---------------------------------------------------------------- MXFP4
+// Workspace of the MXFP4 W4A4 path: X as MXFP4 (codes [M, K/2], E8M0 scales [M, K/32]).
+struct MxA4Layout {
+  size_t off_codes, off_sf, off_x, total;
+};
+MxA4Layout mx_a4_layout(int64_t M, int64_t K) {
+  MxA4Layout L = {};
+  L.off_codes = 0;
+  L.off_sf = align256(size_t(M) * size_t(K / 2));
+  L.off_x = align256(L.off_sf + size_t(M) * size_t(K / 32));
+  L.total = align256(L.off_x + size_t(M) * size_t(K) * 2);
+  return L;
+}
+
+// A kernel launched with programmatic stream serialization (it waits with
+// griddepcontrol.wait before it reads global memory).
+template <typename... Params, typename... Args>
+int launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const char* what,
+               Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...), what);
+}
+
+unsigned mx_grid(uint64_t words) {
+  const uint64_t per = uint64_t(wq::kMxThreads) * wq::kMxUnroll;
+  return unsigned(std::max<uint64_t>(1, std::min<uint64_t>((words + per - 1) / per, 148 * 16)));
+}
+
+int mxfp4_pack_launch(const uint16_t* A, int64_t R, int64_t C, const float* s, uint8_t* codes, uint8_t* bscale,
+                      cudaStream_t st) {
+  const uint64_t words = uint64_t(R) * uint64_t(C / 8);
+  return launch_pdl(wq::mxfp4_pack_kernel, dim3(mx_grid(words)), dim3(wq::kMxThreads), 0, st, "mxfp4_pack launch", A, s,
+                    words, uint32_t(C / 8), reinterpret_cast<uint32_t*>(codes), bscale);
+}
+
+int mxfp4_unpack_launch(const uint8_t* codes, const uint8_t* bscale, int64_t R, int64_t C, uint16_t* out,
+                        cudaStream_t st) {
+  const uint64_t words = uint64_t(R) * uint64_t(C / 8);
+  return launch_pdl(wq::mxfp4_unpack_kernel, dim3(mx_grid(words)), dim3(wq::kMxThreads), 0, st, "mxfp4_unpack launch",
+                    reinterpret_cast<const uint32_t*>(codes), bscale, words, out);
+}
+
+// ---------------------------------------------------------------- experts
+int launch_experts(const wq::ExpertArgs& a, int fmt, cudaStream_t st) {
+  for (int t0 = 0; t0 < 1; ++t0) {
+    const dim3 grid(unsigned((a.N + 7) / 8), unsigned(a.T));
+    if (fmt == WQ_FMT_INT4)
+      wq::experts_simple_kernel<wq::GEMM_INT4><<<grid, 256, 0, st>>>(a);
+    else if (fmt == WQ_FMT_NVFP4)
+      wq::experts_simple_kernel<wq::GEMM_NVFP4><<<grid, 256, 0, st>>>(a);
+    else
+      wq::experts_simple_kernel<wq::GEMM_MXFP4><<<grid, 256, 0, st>>>(a);
+  }
+  return launched("experts launch");
+}
+
 // NVFP4 quantization of a bf16 [R, C] tensor (optionally times s per column)
 // into codes / scales / g: the stream-ordered passes of wq_quantize_nvfp4
 // (zeroing, an atomic amax pass, pack, and a one-thread pass that turns the
@@ -839,6 +907,9 @@ wq::FacGemmArgs fac_args(const double* A, int64_t lda, const double* B, int64_t 
 // Decode GEMV up to this many activation rows, tensor-core GEMM above.
 constexpr int64_t kGemvMaxM = 16;
 
+// Experts of one stack (a CTA keeps their row bounds in shared memory).
+constexpr int kMaxExperts = 1024;
+
 // ---------------------------------------------------------------- fixed scratch
 // Scratch memory of wq_linear_nvfp4_w4a4_noalloc, owned by the library: the
 // NVFP4 pack of X (codes | E4M3 scales | g_x, laid out as w4a4_layout) lives
@@ -903,14 +974,23 @@ int wq_nvfp4_sizes(int64_t N, int64_t K, size_t* codes_bytes, size_t* bscale_byt
   return WQ_OK;
 }
 
+int wq_mxfp4_sizes(int64_t N, int64_t K, size_t* codes_bytes, size_t* bscale_bytes) {
+  if (int e = check_shape(N, K)) return e;
+  if (codes_bytes) *codes_bytes = size_t(N) * size_t(K / 2);
+  if (bscale_bytes) *bscale_bytes = size_t(N) * size_t(K / 32);
+  return WQ_OK;
+}
+
 int wq_linear_workspace_size(int64_t M, int64_t N, int64_t K, int format, int act_fp4, size_t* bytes) {
   REQUIRE(bytes, "bytes must not be NULL");
   REQUIRE(M > 0, "M must be positive");
   if (int e = check_shape(N, K)) return e;
-  REQUIRE(format == WQ_FMT_INT4 || format == WQ_FMT_NVFP4, "unknown format %d", format);
+  REQUIRE(format == WQ_FMT_INT4 || format == WQ_FMT_NVFP4 || format == WQ_FMT_MXFP4, "unknown format %d", format);
   REQUIRE(act_fp4 == 0 || act_fp4 == 1, "act_fp4 must be 0 or 1");
-  REQUIRE(!act_fp4 || format == WQ_FMT_NVFP4, "act_fp4 needs the NVFP4 format");
-  if (act_fp4) {
+  REQUIRE(!act_fp4 || format != WQ_FMT_INT4, "act_fp4 needs the NVFP4 or the MXFP4 format");
+  if (format == WQ_FMT_MXFP4) {
+    *bytes = act_fp4 ? mx_a4_layout(M, K).total : 0;
+  } else if (act_fp4) {
     *bytes = w4a4_layout(M, K).total;
   } else {
     *bytes = M > kGemvMaxM ? gemm_plan(M, N, K).ws_bytes : 0;
@@ -1425,6 +1505,92 @@ int wq_linear_nvfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
   return launch_gemv<wq::FMT_NVFP4>(a, as_stream(stream));
 }
 
+int wq_quantize_mxfp4(const uint16_t* W, int64_t N, int64_t K, const float* scale_s, uint8_t* codes, uint8_t* bscale,
+                      void* stream) {
+  if (int e = check_shape(N, K)) return e;
+  REQUIRE_PTR(W);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(bscale);
+  REQUIRE_OPT_PTR(scale_s);
+  return mxfp4_pack_launch(W, N, K, scale_s, codes, bscale, as_stream(stream));
+}
+
+int wq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* bscale, int64_t N, int64_t K, uint16_t* W, void* stream) {
+  if (int e = check_shape(N, K)) return e;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(bscale);
+  REQUIRE_PTR(W);
+  return mxfp4_unpack_launch(codes, bscale, N, K, W, as_stream(stream));
+}
+
+int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint8_t* codes, const uint8_t* bscale,
+                    int act_fp4, const float* act_inv_s, uint16_t* Y, void* ws, size_t ws_bytes, void* stream) {
+  REQUIRE(M > 0 && M <= (int64_t(1) << 30), "M must be positive");
+  if (int e = check_shape(N, K)) return e;
+  REQUIRE(act_fp4 == 0 || act_fp4 == 1, "act_fp4 must be 0 or 1");
+  REQUIRE_PTR(X);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(bscale);
+  REQUIRE_PTR(Y);
+  REQUIRE_OPT_PTR(act_inv_s);
+  cudaStream_t st = as_stream(stream);
+  wq::ExpertArgs a = {};
+  a.X = X; a.inv_s = act_inv_s; a.packed = codes; a.bscale = bscale; a.Y = Y;
+  a.E = 1; a.N = int(N); a.K = int(K); a.T = int(M);
+  if (act_fp4) {
+    REQUIRE(K % 64 == 0, "W4A4 needs K %% 64 == 0 (got %lld)", (long long)K);
+    const MxA4Layout L = mx_a4_layout(M, K);
+    REQUIRE(ws && ws_bytes >= L.total, "workspace too small: need %zu bytes (wq_linear_workspace_size)", L.total);
+    REQUIRE_PTR(ws);
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    if (int e = mxfp4_pack_launch(X, M, K, act_inv_s, wsb + L.off_codes, wsb + L.off_sf, st)) return e;
+    uint16_t* xv = reinterpret_cast<uint16_t*>(wsb + L.off_x);
+    if (int e = mxfp4_unpack_launch(wsb + L.off_codes, wsb + L.off_sf, M, K, xv, st)) return e;
+    a.X = xv; a.inv_s = nullptr;
+  }
+  return launch_experts(a, WQ_FMT_MXFP4, st);
+}
+
+int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, const int32_t* offsets, uint16_t* Y,
+                      void* stream) {
+  REQUIRE(w, "the expert stack must not be NULL");
+  REQUIRE(w->format == WQ_FMT_INT4 || w->format == WQ_FMT_NVFP4 || w->format == WQ_FMT_MXFP4, "unknown format %d",
+          w->format);
+  REQUIRE(w->E > 0 && w->E <= kMaxExperts, "E must be in 1..%d (got %lld)", kMaxExperts, (long long)w->E);
+  if (int e = check_shape(w->N, w->K)) return e;
+  REQUIRE(w->E * w->N < (int64_t(1) << 31), "E x N must be below 2^31");
+  REQUIRE(T >= 0 && T <= (int64_t(1) << 30), "T must not be negative");
+  if (w->format == WQ_FMT_INT4) {
+    if (int e = check_group(w->group_size, w->K)) return e;
+    REQUIRE(w->zero_point == 0 || w->zero_point == 1, "zero_point must be 0 or 1");
+    REQUIRE_PTR(w->scales);
+    if (w->zero_point) {
+      REQUIRE_PTR(w->zeros);
+    } else {
+      REQUIRE(!w->zeros, "zeros must be NULL for a symmetric (zero_point=0) pack");
+    }
+  } else {
+    REQUIRE_PTR(w->bscale);
+    if (w->format == WQ_FMT_NVFP4)
+      REQUIRE(w->global_scale && (reinterpret_cast<uintptr_t>(w->global_scale) & 3) == 0,
+              "global_scale (one float per expert) must be a 4-byte aligned device pointer");
+  }
+  REQUIRE_PTR(w->packed);
+  if (T == 0) return WQ_OK;  // no rows: nothing to compute, X and Y may be NULL
+  REQUIRE(offsets && (reinterpret_cast<uintptr_t>(offsets) & 3) == 0, "offsets must be a 4-byte aligned device pointer");
+  REQUIRE_PTR(X);
+  REQUIRE_PTR(Y);
+  wq::ExpertArgs a = {};
+  a.X = X; a.offsets = offsets; a.packed = static_cast<const uint8_t*>(w->packed); a.Y = Y;
+  a.E = int(w->E); a.N = int(w->N); a.K = int(w->K); a.T = int(T);
+  if (w->format == WQ_FMT_INT4) {
+    a.scales = w->scales; a.zeros = w->zeros; a.log2g = log2i(w->group_size);
+  } else {
+    a.bscale = w->bscale; a.gscale = w->format == WQ_FMT_NVFP4 ? w->global_scale : nullptr;
+  }
+  return launch_experts(a, w->format, as_stream(stream));
+}
+
 namespace {
 TcCall tc_call_of(const wq_linear_item& it) {
   const bool int4 = it.format == WQ_FMT_INT4;
@@ -1439,7 +1605,8 @@ int check_items(const wq_linear_item* items, int count, int64_t M) {
   REQUIRE(M > 0 && M <= 16, "wq_linear_group serves decode sizes: 1 <= M <= 16 (got %lld)", (long long)M);
   for (int i = 0; i < count; ++i) {
     const wq_linear_item& it = items[i];
-    REQUIRE(it.format == WQ_FMT_INT4 || it.format == WQ_FMT_NVFP4, "item %d: unknown format %d", i, it.format);
+    REQUIRE(it.format == WQ_FMT_INT4 || it.format == WQ_FMT_NVFP4 || it.format == WQ_FMT_MXFP4,
+            "item %d: unknown format %d", i, it.format);
     if (int e = check_shape(it.N, it.K)) return e;
     REQUIRE_PTR(it.X);
     REQUIRE_PTR(it.packed);
@@ -1452,7 +1619,7 @@ int check_items(const wq_linear_item* items, int count, int64_t M) {
       if (it.zero_point) REQUIRE_PTR(it.zeros);
     } else {
       REQUIRE_PTR(it.bscale);
-      REQUIRE_PTR(it.global_scale);
+      if (it.format == WQ_FMT_NVFP4) REQUIRE_PTR(it.global_scale);
     }
   }
   return WQ_OK;
@@ -1470,7 +1637,7 @@ int wq_linear_group(const wq_linear_item* items, int count, int64_t M, void* str
     std::vector<int> kinds(static_cast<size_t>(count));
     for (int i = 0; i < count; ++i) {
       calls[size_t(i)] = tc_call_of(items[i]);
-      kinds[size_t(i)] = tc_kind(calls[size_t(i)], M);
+      kinds[size_t(i)] = items[i].format == WQ_FMT_MXFP4 ? -1 : tc_kind(calls[size_t(i)], M);
     }
     if (int e = run_tc(calls.data(), kinds.data(), count, M, st, done.data())) return e;
   }
@@ -1481,6 +1648,9 @@ int wq_linear_group(const wq_linear_item* items, int count, int64_t M, void* str
                       ? wq_linear_int4(it.X, M, it.N, it.K, static_cast<const uint32_t*>(it.packed), it.scales,
                                        it.zero_point ? it.zeros : nullptr, it.group_size, it.zero_point, it.act_inv_s,
                                        it.Y, nullptr, 0, stream)
+                  : it.format == WQ_FMT_MXFP4
+                      ? wq_linear_mxfp4(it.X, M, it.N, it.K, static_cast<const uint8_t*>(it.packed), it.bscale, 0,
+                                        it.act_inv_s, it.Y, nullptr, 0, stream)
                       : wq_linear_nvfp4(it.X, M, it.N, it.K, static_cast<const uint8_t*>(it.packed), it.bscale,
                                         it.global_scale, 0, it.act_inv_s, it.Y, nullptr, 0, stream);
     if (e) return e;
@@ -1537,8 +1707,10 @@ int wq_device_error(void* stream) {
   if (word == wq::ERR_NOT_POSITIVE_DEFINITE)
     return fail(WQ_ERR_ARG, "GPTQ Hessian factor: the damped Hessian is not positive definite "
                             "(non-finite calibration tokens?); U holds NaN");
+  if (word == wq::ERR_OFFSETS)
+    return fail(WQ_ERR_ARG, "expert offsets decrease or leave [0, T]: nothing was computed");
   return fail(WQ_ERR_TIMEOUT, "device error word 0x%x (1=TMA wait, 2=MMA wait, 4=pipeline wait, 8=bounds, "
-                              "16=Hessian not positive definite)", word);
+                              "16=Hessian not positive definite, 32=expert offsets)", word);
 }
 
 }  // extern "C"

@@ -12,6 +12,7 @@ enum : unsigned {
   ERR_TIMEOUT_MMA = 1u << 1,   // a wait for tensor-core completion ran out
   ERR_TIMEOUT_PIPE = 1u << 2,  // a wait between producer / consumer warps ran out
   ERR_BOUNDS = 1u << 3,        // a kernel skipped an access that would leave its buffers
+  ERR_OFFSETS = 1u << 5,       // expert offsets that decrease or leave [0, T] (bit 4: gptq_factor.cuh)
 };
 
 // One word per GPU that loads the library.
