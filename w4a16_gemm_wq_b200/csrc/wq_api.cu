@@ -575,17 +575,60 @@ int mxfp4_unpack_launch(const uint8_t* codes, const uint8_t* bscale, int64_t R, 
 }
 
 // ---------------------------------------------------------------- experts
-int launch_experts(const wq::ExpertArgs& a, int fmt, cudaStream_t st) {
-  for (int t0 = 0; t0 < 1; ++t0) {
-    const dim3 grid(unsigned((a.N + 7) / 8), unsigned(a.T));
-    if (fmt == WQ_FMT_INT4)
-      wq::experts_simple_kernel<wq::GEMM_INT4><<<grid, 256, 0, st>>>(a);
-    else if (fmt == WQ_FMT_NVFP4)
-      wq::experts_simple_kernel<wq::GEMM_NVFP4><<<grid, 256, 0, st>>>(a);
-    else
-      wq::experts_simple_kernel<wq::GEMM_MXFP4><<<grid, 256, 0, st>>>(a);
+template <int FMT, typename S>
+int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed, int split, int64_t items,
+                        cudaStream_t st) {
+  if (int e = make_tmap_2d(&a.tmW, packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.E) * uint64_t(a.N),
+                           uint64_t(a.K / 2), 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  if (int e = make_tmap_2d(&a.tmX, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(a.T), uint64_t(a.K), S::XBOX, 64,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  static std::atomic<uint64_t> attr_done{0};
+  if (int e = ensure_smem_attr(wq::expert_gemm_kernel<FMT, S>, S::SMEM_BYTES, &attr_done, "expert smem attribute"))
+    return e;
+  a.split = split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(split > 1 ? items * split : std::min<int64_t>(items, wq::kTcMaxCtas)), 1, 1);
+  cfg.blockDim = dim3(wq::kExpThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  if (split > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = split;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
   }
-  return launched("experts launch");
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
+}
+
+template <int FMT>
+int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* packed, cudaStream_t st) {
+  // the host does not know how the rows fall on the experts: at most min(E, T) hold any, and
+  // each adds at most one partly filled tile
+  const int64_t holders = std::min(a.E, a.T);
+  const auto items = [&](int wt, int xt) {
+    return (holders + a.T / xt) * ((int64_t(a.N) + 128 * wt - 1) / (128 * wt));
+  };
+  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(2, 192), st);
+  const int64_t n = items(1, 64);
+  const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
+  const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
+  return launch_expert_shape<FMT, wq::ExpNarrow>(a, X, packed, split, n, st);
+}
+
+int launch_experts(const wq::ExpertArgs& a, int fmt, const uint16_t* X, const void* packed, cudaStream_t st) {
+  return fmt == WQ_FMT_INT4    ? launch_experts_fmt<wq::GEMM_INT4>(a, X, packed, st)
+         : fmt == WQ_FMT_NVFP4 ? launch_experts_fmt<wq::GEMM_NVFP4>(a, X, packed, st)
+                               : launch_experts_fmt<wq::GEMM_MXFP4>(a, X, packed, st);
 }
 
 // NVFP4 quantization of a bf16 [R, C] tensor (optionally times s per column)
@@ -906,9 +949,6 @@ wq::FacGemmArgs fac_args(const double* A, int64_t lda, const double* B, int64_t 
 
 // Decode GEMV up to this many activation rows, tensor-core GEMM above.
 constexpr int64_t kGemvMaxM = 16;
-
-// Experts of one stack (a CTA keeps their row bounds in shared memory).
-constexpr int kMaxExperts = 1024;
 
 // ---------------------------------------------------------------- fixed scratch
 // Scratch memory of wq_linear_nvfp4_w4a4_noalloc, owned by the library: the
@@ -1535,7 +1575,7 @@ int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
   REQUIRE_OPT_PTR(act_inv_s);
   cudaStream_t st = as_stream(stream);
   wq::ExpertArgs a = {};
-  a.X = X; a.inv_s = act_inv_s; a.packed = codes; a.bscale = bscale; a.Y = Y;
+  a.inv_s = act_inv_s; a.bscale = bscale; a.Y = Y;
   a.E = 1; a.N = int(N); a.K = int(K); a.T = int(M);
   if (act_fp4) {
     REQUIRE(K % 64 == 0, "W4A4 needs K %% 64 == 0 (got %lld)", (long long)K);
@@ -1546,9 +1586,10 @@ int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
     if (int e = mxfp4_pack_launch(X, M, K, act_inv_s, wsb + L.off_codes, wsb + L.off_sf, st)) return e;
     uint16_t* xv = reinterpret_cast<uint16_t*>(wsb + L.off_x);
     if (int e = mxfp4_unpack_launch(wsb + L.off_codes, wsb + L.off_sf, M, K, xv, st)) return e;
-    a.X = xv; a.inv_s = nullptr;
+    X = xv;
+    a.inv_s = nullptr;
   }
-  return launch_experts(a, WQ_FMT_MXFP4, st);
+  return launch_experts(a, WQ_FMT_MXFP4, X, codes, st);
 }
 
 int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, const int32_t* offsets, uint16_t* Y,
@@ -1556,7 +1597,7 @@ int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, co
   REQUIRE(w, "the expert stack must not be NULL");
   REQUIRE(w->format == WQ_FMT_INT4 || w->format == WQ_FMT_NVFP4 || w->format == WQ_FMT_MXFP4, "unknown format %d",
           w->format);
-  REQUIRE(w->E > 0 && w->E <= kMaxExperts, "E must be in 1..%d (got %lld)", kMaxExperts, (long long)w->E);
+  REQUIRE(w->E > 0 && w->E <= wq::kMaxExperts, "E must be in 1..%d (got %lld)", wq::kMaxExperts, (long long)w->E);
   if (int e = check_shape(w->N, w->K)) return e;
   REQUIRE(w->E * w->N < (int64_t(1) << 31), "E x N must be below 2^31");
   REQUIRE(T >= 0 && T <= (int64_t(1) << 30), "T must not be negative");
@@ -1581,14 +1622,14 @@ int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, co
   REQUIRE_PTR(X);
   REQUIRE_PTR(Y);
   wq::ExpertArgs a = {};
-  a.X = X; a.offsets = offsets; a.packed = static_cast<const uint8_t*>(w->packed); a.Y = Y;
+  a.offsets = offsets; a.Y = Y;
   a.E = int(w->E); a.N = int(w->N); a.K = int(w->K); a.T = int(T);
   if (w->format == WQ_FMT_INT4) {
     a.scales = w->scales; a.zeros = w->zeros; a.log2g = log2i(w->group_size);
   } else {
     a.bscale = w->bscale; a.gscale = w->format == WQ_FMT_NVFP4 ? w->global_scale : nullptr;
   }
-  return launch_experts(a, w->format, as_stream(stream));
+  return launch_experts(a, w->format, X, w->packed, as_stream(stream));
 }
 
 namespace {
