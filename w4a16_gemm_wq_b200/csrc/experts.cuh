@@ -2,26 +2,27 @@
 // on the 5th-generation tensor cores, and the MXFP4 Linear (one expert):
 //   Y[i] = X[i] W_e^T   for offsets[e] <= i < offsets[e + 1]
 //
-// The weights are the M side of the MMA (128 rows of W_e per accumulator), the
-// rows of X its N side: the instruction's N is a run-time value, so that a tile
-// takes the rows that an expert has (rounded up to 16) instead of padding them to
-// a tile, and a few rows per expert cost a few columns of MMA.
+// The weights are the M side of the MMA (128 rows of W_e), the rows of X its N
+// side: the instruction's N is a run-time value, so that a tile takes the rows
+// that an expert has (rounded up to 16) instead of padding them to a tile, and a
+// few rows per expert cost a few columns of MMA.
 //
 // The packed weights are dequantized straight into tensor memory: a
 // dequantizer thread owns one weight row (one TMEM lane), turns 64 codes into 32
 // words of bf16 pairs in registers and stores them with one tcgen05.st; the MMA
 // reads them as its A operand.  The dequantized weights never pass through
-// shared memory, whose bandwidth (writes and reads of X and of the codes) is
-// what bounds the kernel at large T.
+// shared memory.
 //
-// One CTA walks items (expert, row tile, 128 WT weight rows).  Roles:
-//   warp 0       codes [128 WT x 256 k] by TMA, with the rows' scales and zero
-//                points by cp.async, into a ring of WS stages
+// One CTA walks items (expert, row tile, 128 weight rows).  Roles:
+//   warp 0       codes [128 x 256 k] by TMA, with the rows' scales and zero points
+//                by cp.async, into a ring of WS stages
 //   warp 1       X boxes [XBOX rows x 64 k] by TMA into a ring of XS slots
-//   warp 2       TMEM allocation and the MMA issuer
-//   warps 4-11   dequantizers (WT = 2: four warps per weight tile; WT = 1: the two
-//                groups of four warps take alternate k-blocks)
-//   warps 12-15  epilogue: tcgen05.ld, transpose in shared memory, store Y
+//   warp 2       TMEM allocation and the MMA issuer (a whole warp in step, one
+//                elected lane issues: a lone lane's branch costs 46 clocks an
+//                instruction against 9 measured here)
+//   warps 4-19   dequantizers: four groups of four warps, one 64-wide k-block of
+//                every four each, into its own 32 columns of tensor memory
+//   warps 20-23  epilogue: tcgen05.ld, transpose in shared memory, store Y
 // All waits are bounded; see mbar_wait.
 #pragma once
 
@@ -34,7 +35,7 @@
 namespace wq {
 
 constexpr int kMaxExperts = 1024;  // a CTA keeps the experts' row bounds in shared memory
-constexpr int kExpThreads = 512;
+constexpr int kExpThreads = 768;
 constexpr int kExpChunk = 256;     // k per stage of codes (128 bytes a row)
 
 struct ExpertArgs {
@@ -52,33 +53,34 @@ struct ExpertArgs {
   int split;               // CTAs of a cluster that share an item along K (1: none)
 };
 
-// WT weight tiles of 128 rows, up to XT rows of X per item, NACC accumulators
-// per weight tile (2: the epilogue overlaps the next item), AS stages of
-// dequantized weights in tensor memory (32 columns per tile each).
-template <int WT_, int XT_, int XBOX_, int NACC_, int AS_, int WS_, int XS_>
+constexpr int kExpGroups = 4;      // dequantizer groups, and stages of dequantized weights (32 columns each)
+
+// Up to XT rows of X per item, in boxes of XBOX; NACC accumulators (2: the
+// epilogue overlaps the next item); WS stages of codes, XS slots of X.
+template <int XT_, int XBOX_, int NACC_, int WS_, int XS_>
 struct ExpShape {
-  static constexpr int WT = WT_, XT = XT_, XBOX = XBOX_, NACC = NACC_, AS = AS_, WS = WS_, XS = XS_;
-  static constexpr int CODE_BYTES = WT * 128 * 128;
-  static constexpr int META_BYTES = WT * 128 * 24;  // per row 16 bytes of scales, a fifth word, a word of zero points
+  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_;
+  static constexpr int CODE_BYTES = 128 * 128;
+  static constexpr int META_BYTES = 128 * 24;  // per row 16 bytes of scales, a fifth word, a word of zero points
   static constexpr int SLOT_BYTES = XT * 128;
   static constexpr int OFF_X = WS * CODE_BYTES;
   static constexpr int OFF_META = OFF_X + XS * SLOT_BYTES;
   static constexpr int OFF_STAGE = OFF_META + WS * META_BYTES;
   static constexpr int OFF_TAB = OFF_STAGE + 4 * 1024;
   static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxExperts + 4) * 4;
-  static constexpr int NBAR = 2 * WS + 2 * XS + 2 * AS + 2 * NACC;
+  static constexpr int NBAR = 2 * WS + 2 * XS + kExpGroups + 2 * NACC;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 64 + 1024;
-  static constexpr int ACC_COLS = WT * XT;
-  static constexpr int A_COL = NACC * ACC_COLS;
-  static constexpr int USED_COLS = A_COL + AS * WT * 32;
-  static constexpr int TMEM_COLS = USED_COLS <= 128 ? 128 : USED_COLS <= 256 ? 256 : 512;
+  static constexpr int A_COL = NACC * XT;
+  static constexpr int USED_COLS = A_COL + kExpGroups * 32;
+  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static_assert(USED_COLS <= 512, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(XT % 16 == 0 && XT <= 256 && XT % XBOX == 0 && XBOX % 8 == 0, "row tiles");
+  static_assert(XS >= kExpGroups, "a dequantizer waits for the k-block four back on the slots' barriers");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
-using ExpWide = ExpShape<2, 192, 32, 1, 2, 3, 4>;
-using ExpNarrow = ExpShape<1, 64, 8, 2, 4, 6, 8>;
+using ExpWide = ExpShape<192, 32, 2, 4, 5>;
+using ExpNarrow = ExpShape<64, 8, 2, 6, 8>;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -118,102 +120,83 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack_b32x2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_of(uint64_t p) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-  return pack_bf16x2(lo, hi);
+// One lane of a converged warp: the compiler then knows the branch's warp to be in step.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
 }
 
-// INT4: (q - z) s of the 8 codes of a word, natural order, rounded to bf16 once.
-// A nibble at bits 12-15 (or 16-19) under the exponent of 2^23 is the fp32 value
-// 2^23 + 2^12 q; one fused multiply-add by 2^-12 s and -(2^11 + z) s (exact: 12 by
-// 11 bits) gives (q - z) s exactly (15 bits).
-struct Int4Consts {
-  uint64_t m33, c33, m43, c43;  // {bits 12-15, bits 12-15} and {bits 16-19, bits 12-15}
-};
-__device__ __forceinline__ Int4Consts int4_consts(float s, float z) {
-  const float m3 = s * 0x1p-12f, m4 = s * 0x1p-16f, c3 = -(2048.f + z) * s, c4 = -(128.f + z) * s;
-  return Int4Consts{pack_f32x2(m3, m3), pack_f32x2(c3, c3), pack_f32x2(m4, m3), pack_f32x2(c4, c3)};
-}
-__device__ __forceinline__ void dequant8_int4(uint32_t w, const Int4Consts& k, uint32_t* out) {
-  constexpr uint32_t B = 0x4B000000u, N3 = 0xF000u, N4 = 0xF0000u;
-  const uint32_t l12 = w << 12, l8 = w << 8, r8 = w >> 8, r16 = w >> 16;
-  out[0] = bf16x2_of(fma_f32x2(pack_b32x2(lop3_andor(l12, N3, B), lop3_andor(l8, N3, B)), k.m33, k.c33));
-  out[1] = bf16x2_of(fma_f32x2(pack_b32x2(lop3_andor(l8, N4, B), lop3_andor(w, N3, B)), k.m43, k.c43));
-  out[2] = bf16x2_of(fma_f32x2(pack_b32x2(lop3_andor(w, N4, B), lop3_andor(r8, N3, B)), k.m43, k.c43));
-  out[3] = bf16x2_of(fma_f32x2(pack_b32x2(lop3_andor(r8, N4, B), lop3_andor(r16, N3, B)), k.m43, k.c43));
-}
-
-// E2M1: the 8 codes of a word as bf16 pairs e2m1 2^-126, natural order: the code's
-// sign at bit 15 and its three low bits at bits 8-6 are that bf16 (0.5 is its
-// subnormal), times mul2 = {m, m} (exact: at most 6 significant bits).
-__device__ __forceinline__ void dequant8_e2m1(uint32_t w, uint32_t mul2, uint32_t* out) {
-  const uint32_t w4 = w << 4;
+// The integer pipe that shifts, masks and permutes runs at half the rate of the
+// multiply-add pipe, and bounds the dequantization: both forms below move what they
+// can to multiply-adds.
+//
+// INT4: (q - z) s of the 8 codes of a word in natural order.  d = (128 + q) - (128 + z)
+// is exact in bf16; the fp16 scale is the exact sum of two bf16, s = hi + lo, and
+// fma(d, hi, d lo) rounds to bf16 once (d lo's own rounding is 2^-9 of 2^-9 of the
+// value).
+__device__ __forceinline__ void dequant8_int4(uint32_t w, uint32_t z128, uint32_t hi, uint32_t lo, uint32_t* out) {
+  uint32_t p[4];  // {code i, code i + 4}
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // byte 1 = byte i of w4 (code 2i in its high nibble), byte 3 = byte i of w (code 2i + 1)
-    const uint32_t r = prmt_b32(w4, w, uint32_t(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
-    const uint32_t x = (r >> 6) & 0x01C001C0u;
-    out[i] = bf16x2_mul(lop3_andor(r, 0x80008000u, x), mul2);
+    const uint32_t d = bf16x2_sub(lop3_andor(w >> (4 * i), 0x000F000Fu, 0x43004300u), z128);
+    p[i] = bf16x2_fma(d, hi, bf16x2_mul(d, lo));
+  }
+  out[0] = prmt_b32(p[0], p[1], 0x5410);
+  out[1] = prmt_b32(p[2], p[3], 0x5410);
+  out[2] = prmt_b32(p[0], p[1], 0x7632);
+  out[3] = prmt_b32(p[2], p[3], 0x7632);
+}
+
+// E2M1: the 8 codes of a word as bf16 pairs e2m1 2^-126 in natural order, times
+// mul2 = {m, m} (exact: at most 6 significant bits).  A code's sign at bit 15 and its
+// three low bits at bits 8-6 are that bf16 (0.5 is its subnormal): the code times 64
+// puts the low bits there and the sign at bit 9, and sign (4096 - 64) moves it to bit 15.
+__device__ __forceinline__ void dequant8_e2m1(uint32_t w, uint32_t mul2, uint32_t* out) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // {code 2i, code 2i + 1}, zero-extended: a selector with bit 3 set replicates the byte's top bit, which is 0
+    const uint32_t r = prmt_b32(even, odd, uint32_t(i | ((i | 8) << 4) | ((4 + i) << 8) | ((4 + i + 8) << 12)));
+    out[i] = bf16x2_mul(r * 64u + (r & 0x00080008u) * 4032u, mul2);
   }
 }
 
 template <int FMT, typename S>
 __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertArgs a) {
-  constexpr int WT = S::WT, XT = S::XT, AS = S::AS, WS = S::WS, XS = S::XS, NACC = S::NACC;
+  constexpr int XT = S::XT, WS = S::WS, XS = S::XS, NACC = S::NACC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   int* bound = reinterpret_cast<int*>(smem + S::OFF_TAB);  // [E + 1] rows of the experts
   int* tstart = bound + kMaxExperts + 4;                   // [E + 1] their first row tile
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-  uint64_t* wfull = bars;             // codes and scales landed
-  uint64_t* wempty = wfull + WS;      // dequantizers are done with them
-  uint64_t* xfull = wempty + WS;      // X boxes landed
-  uint64_t* xempty = xfull + XS;      // MMAs of the slot finished
-  uint64_t* aready = xempty + XS;     // dequantized weights in tensor memory
-  uint64_t* aempty = aready + AS;     // MMAs of the stage finished
-  uint64_t* dfull = aempty + AS;      // accumulator complete
-  uint64_t* dempty = dfull + NACC;    // accumulator drained
+  uint64_t* wfull = bars;                 // codes and scales landed
+  uint64_t* wempty = wfull + WS;          // dequantizers are done with them
+  uint64_t* xfull = wempty + WS;          // X boxes landed
+  uint64_t* mdone = xfull + XS;           // MMAs of the k-block in this slot finished
+  uint64_t* aready = mdone + XS;          // dequantized weights in tensor memory
+  uint64_t* dfull = aready + kExpGroups;  // accumulator complete
+  uint64_t* dempty = dfull + NACC;        // accumulator drained
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + NACC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* scan = reinterpret_cast<int*>(smem + S::OFF_STAGE);  // [17], before the epilogue uses it
+  int* scan = reinterpret_cast<int*>(smem + S::OFF_STAGE);  // [24], before the epilogue uses it
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < WS; ++s) {
-      mbar_init(&wfull[s], 33);  // the TMA's thread and the 32 lanes that copy the scales
-      mbar_init(&wempty[s], 8);
-    }
-    for (int s = 0; s < XS; ++s) {
-      mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
-    }
-    for (int s = 0; s < AS; ++s) {
-      mbar_init(&aready[s], 4 * WT);
-      mbar_init(&aempty[s], 1);
-    }
-    for (int s = 0; s < NACC; ++s) {
-      mbar_init(&dfull[s], 1);
-      mbar_init(&dempty[s], 4);
-    }
-    *abort_flag = 0;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x < S::NBAR) {
+    // arrivals: codes = the TMA's thread and the 32 lanes that copy the scales; one arrival a warp elsewhere
+    const int b = threadIdx.x;
+    mbar_init(&bars[b], b < WS ? 33 : b < 2 * WS ? 4 * kExpGroups : b < 2 * (WS + XS) ? 1
+                        : b < 2 * (WS + XS) + kExpGroups ? 4 : b < 2 * (WS + XS) + kExpGroups + NACC ? 1 : 4);
     fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
     prefetch_tmap(&a.tmW);
     prefetch_tmap(&a.tmX);
   }
@@ -257,15 +240,11 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
         tstart[e0 + j] = before;
         before += t[j];
       }
-    if (e0 + 2 == a.E && threadIdx.x == kExpThreads - 1) {  // E = 1024: the last entry has no thread of its own
-      bound[a.E] = b[2];
-      tstart[a.E] = before;
-    }
     __syncthreads();
   }
   const uint32_t tmem = *tmem_slot;
   if (bad && threadIdx.x == 0 && blockIdx.x == 0) report_error(ERR_OFFSETS);
-  const int nblocks = (a.N + 128 * WT - 1) / (128 * WT);
+  const int nblocks = (a.N + 127) >> 7;
   const int items = bad ? 0 : tstart[a.E] * nblocks;
   const int nchunks = (a.K + kExpChunk - 1) / kExpChunk;
   const int rank = a.split > 1 ? int(cluster_ctarank()) : 0;
@@ -273,12 +252,12 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
 
   struct Item {
-    int e, row, rows, width, n0, tiles;  // rows of X, their number, the MMA's N; first weight row, weight tiles
+    int e, row, rows, n0;  // expert, first row of X and their number, first weight row
   };
   const auto item_of = [&](int id) {
     Item it;
     const int tt = id / nblocks;
-    it.n0 = (id - tt * nblocks) * 128 * WT;
+    it.n0 = (id - tt * nblocks) * 128;
     int lo = 0, hi = a.E;  // the last e with tstart[e] <= tt
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -289,16 +268,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     const int w = ((r + t - 1) / t + 15) & ~15;  // the expert's rows, evenly over its tiles
     it.row = bound[lo] + (tt - tstart[lo]) * w;
     it.rows = min(w, bound[lo + 1] - it.row);
-    it.width = (it.rows + 15) & ~15;
-    it.tiles = (WT == 2 && it.n0 + 128 < a.N) ? 2 : 1;
     return it;
   };
+  const auto kblocks_of = [&](int c) { return min(4, (a.K - c * kExpChunk + 63) >> 6); };
   // a row's scale bytes, those of a chunk, and the largest alignment that all chunks of all rows share
   const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
   const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
   const int sc_want = FMT == GEMM_INT4 ? (kExpChunk >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 16 : 8;
   const int sc_align = (sc_stride | sc_want) & -(sc_stride | sc_want);
-  const auto kblocks_of = [&](int c) { return min(4, (a.K - c * kExpChunk + 63) >> 6); };
 
   if (warp == 0) {
     // ---------------------------------------------------------- codes and scales
@@ -312,13 +289,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
         if (r > 0) ok = mbar_wait(&wempty[s], (r - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&wfull[s], uint32_t(it.tiles) * 16384u);
-          for (int t = 0; t < it.tiles; ++t)
-            tma_load_2d(smem + s * S::CODE_BYTES + t * 16384, &a.tmW, &wfull[s], c * 128, int(row0) + 128 * t);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&wfull[s], uint32_t(S::CODE_BYTES));
+          tma_load_2d(smem + s * S::CODE_BYTES, &a.tmW, &wfull[s], c * 128, int(row0));
         }
+        __syncwarp();
         const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
-        for (int t = lane; t < 128 * it.tiles; t += 32) {
+#pragma unroll 1
+        for (int t = lane; t < 128; t += 32) {
           const int64_t row = row0 + min(t, a.N - 1 - it.n0);
           // the row's scale bytes of this chunk; those past the row's end arrive as zeros
           const uint8_t* src = sc_base + row * sc_stride + int64_t(c) * sc_want;
@@ -327,21 +305,24 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
           if (sc_align == 16) {
             cp_async_zfill<16>(dst, src, uint32_t(have));
           } else if (sc_align == 8) {
-            for (int b = 0; b < sc_want; b += 8) cp_async_zfill<8>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(8, have - b))));
+            for (int b = 0; b < sc_want; b += 8)
+              cp_async_zfill<8>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(8, have - b))));
           } else if (sc_align == 4) {
-            for (int b = 0; b < sc_want; b += 4) cp_async_zfill<4>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(4, have - b))));
+            for (int b = 0; b < sc_want; b += 4)
+              cp_async_zfill<4>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(4, have - b))));
           } else {
             // rows that start inside a word: the words around the bytes, which the dequantizer shifts
             const int off = int(reinterpret_cast<uintptr_t>(src) & 3);
             for (int b = 0; b <= sc_want; b += 4) {
               const int n = max(0, min(4, off + have - b));
-              cp_async_zfill<4>(b < 16 ? dst + b : meta + uint32_t(WT * 128 * 16 + t * 4), src - off + (n ? b : 0), uint32_t(n));
+              cp_async_zfill<4>(b < 16 ? dst + b : meta + uint32_t(128 * 16 + t * 4), src - off + (n ? b : 0),
+                                uint32_t(n));
             }
           }
           if (FMT == GEMM_INT4 && a.zeros) {
             const int ng = a.K >> a.log2g, zw = (ng + 7) >> 3;
             const int word = (c * (kExpChunk >> a.log2g)) >> 3;
-            cp_async_zfill<4>(meta + uint32_t(WT * 128 * 20 + t * 4), a.zeros + row * zw + word, 4);
+            cp_async_zfill<4>(meta + uint32_t(128 * 20 + t * 4), a.zeros + row * zw + word, 4);
           }
         }
         cp_async_arrive(&wfull[s]);
@@ -352,182 +333,197 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- rows of X
-    if (lane == 0) {
-      int q = 0;
-      bool ok = true;
-      for (int id = first; id < items && ok; id += step) {
-        const Item it = item_of(id);
-        const int boxes = (it.rows + S::XBOX - 1) / S::XBOX;
-        for (int c = c0; c < c1 && ok; ++c) {
-          const int nkb = kblocks_of(c);
-          for (int kb = 0; kb < nkb; ++kb, ++q) {
-            const int s = q % XS, r = q / XS;
-            if (r > 0 && !mbar_wait(&xempty[s], (r - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag)) { ok = false; break; }
+    int q = 0, s = 0;
+    uint32_t par = 1;  // parity of the slot's last use (the first use waits for none)
+    bool ok = true;
+    for (int id = first; id < items && ok; id += step) {
+      const Item it = item_of(id);
+      const int boxes = (it.rows + S::XBOX - 1) / S::XBOX;
+      for (int c = c0; c < c1 && ok; ++c) {
+        const int nkb = kblocks_of(c);
+        for (int kb = 0; kb < nkb; ++kb, ++q) {
+          if (q >= XS) ok = mbar_wait(&mdone[s], par, ERR_TIMEOUT_PIPE, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (elect_one()) {
             mbar_arrive_expect_tx(&xfull[s], uint32_t(boxes * S::XBOX) * 128u);
             for (int b = 0; b < boxes; ++b)
               tma_load_2d(smem + S::OFF_X + s * S::SLOT_BYTES + b * S::XBOX * 128, &a.tmX, &xfull[s],
                           c * kExpChunk + kb * 64, it.row + b * S::XBOX);
           }
+          __syncwarp();
+          if (++s == XS) {
+            s = 0;
+            par ^= 1u;
+          }
         }
       }
-      if (!ok) {
-        for (int k = (q > XS ? q - XS : 0); k < q; ++k) mbar_wait(&xfull[k % XS], (k / XS) & 1, ERR_TIMEOUT_TMA, nullptr);
-      }
+    }
+    if (!ok) {
+      for (int k = (q > XS ? q - XS : 0); k < q; ++k) mbar_wait(&xfull[k % XS], (k / XS) & 1, ERR_TIMEOUT_TMA, nullptr);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int q = 0, i = 0;
-      bool ok = true;
-      for (int id = first; id < items && ok; id += step, ++i) {
-        const Item it = item_of(id);
-        const uint32_t idesc = idesc_bf16_f32(128, it.width);
-        const int b = i % NACC, u = i / NACC;
-        if (u > 0 && !mbar_wait(&dempty[b], (u - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t acc = tmem + uint32_t(b * S::ACC_COLS);
-        int nk = 0;
-        for (int c = c0; c < c1 && ok; ++c) {
-          const int nkb = kblocks_of(c);
-          for (int kb = 0; kb < nkb; ++kb, ++q, ++nk) {
-            const int as = q % AS, xs = q % XS;
-            if (!mbar_wait(&xfull[xs], (q / XS) & 1, ERR_TIMEOUT_TMA, abort_flag) ||
-                !mbar_wait(&aready[as], (q / AS) & 1, ERR_TIMEOUT_PIPE, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t xd = desc_kmajor_sw128(sbase + uint32_t(S::OFF_X + xs * S::SLOT_BYTES));
-            for (int t = 0; t < it.tiles; ++t) {
-              const uint32_t at = tmem + uint32_t(S::A_COL + (as * WT + t) * 32);
+    int q = 0, i = 0, xs = 0;
+    uint32_t xpar = 0;
+    bool ok = true;
+    for (int id = first; id < items && ok; id += step, ++i) {
+      const Item it = item_of(id);
+      const uint32_t idesc = idesc_bf16_f32(128, (it.rows + 15) & ~15);
+      const int b = i % NACC, u = i / NACC;
+      if (u > 0) ok = mbar_wait(&dempty[b], (u - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + uint32_t(b * XT);
+      uint32_t more = 0;
+      for (int c = c0; c < c1 && ok; ++c) {
+        const int nkb = kblocks_of(c);
+        for (int kb = 0; kb < nkb; ++kb, ++q) {
+          const int as = q % kExpGroups;
+          ok = mbar_wait(&xfull[xs], xpar, ERR_TIMEOUT_TMA, abort_flag) &&
+               mbar_wait(&aready[as], (q / kExpGroups) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t xd = desc_kmajor_sw128(sbase + uint32_t(S::OFF_X + xs * S::SLOT_BYTES));
+          const uint32_t at = tmem + uint32_t(S::A_COL + as * 32);
+          if (elect_one()) {
 #pragma unroll
-              for (int k4 = 0; k4 < 4; ++k4)  // K = 16: 8 columns of A, 32 bytes inside X's swizzle atom
-                umma_bf16_ts(acc + uint32_t(t * XT), at + uint32_t(8 * k4), xd + uint64_t(2 * k4), idesc,
-                             (nk | k4) != 0);
-            }
-            umma_commit(&aempty[as]);
-            umma_commit(&xempty[xs]);
+            for (int k4 = 0; k4 < 4; ++k4)  // K = 16: 8 columns of A, 32 bytes inside X's swizzle atom
+              umma_bf16_ts(acc, at + uint32_t(8 * k4), xd + uint64_t(2 * k4), idesc, more | uint32_t(k4));
+            umma_commit(&mdone[xs]);
+          }
+          __syncwarp();
+          more = 1;
+          if (++xs == XS) {
+            xs = 0;
+            xpar ^= 1u;
           }
         }
-        umma_commit(&dfull[b]);  // also after an abort: completes when the issued MMAs are done
       }
+      if (elect_one()) umma_commit(&dfull[b]);  // also after an abort: completes when the issued MMAs are done
+      __syncwarp();
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + 4 * kExpGroups) {
     // ---------------------------------------------------------- dequantizers
-    const int grp = (warp - 4) >> 2;      // WT = 2: weight tile; WT = 1: parity of the k-blocks
-    const int quarter = warp & 3;         // TMEM lanes of this warp
-    const int trow = quarter * 32 + lane; // weight row within the tile
-    const uint32_t lane_base = uint32_t(quarter * 32) << 16;
-    const int tile = WT == 2 ? grp : 0;
-    int q = 0, qk = 0;  // chunks and k-blocks so far
+    const int grp = (warp - 4) >> 2;       // takes the k-blocks q with q % 4 == grp
+    const int quarter = warp & 3;          // TMEM lanes of this warp
+    const int trow = quarter * 32 + lane;  // weight row within the tile
+    const uint32_t a_tmem = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(S::A_COL + grp * 32);
+    int s = 0, q = 0;
+    uint32_t wpar = 0;
     bool ok = true;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
-      for (int c = c0; c < c1 && ok; ++c, ++q) {
-        const int s = q % WS;
+      for (int c = c0; c < c1; ++c) {
         const int nkb = kblocks_of(c);
-        ok = mbar_wait(&wfull[s], (q / WS) & 1, ERR_TIMEOUT_TMA, abort_flag);
+        ok = mbar_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t codes = sbase + uint32_t(s * S::CODE_BYTES + tile * 16384 + trow * 128);
+        const int kb = (grp - q) & (kExpGroups - 1);  // this group's k-block of the chunk
         const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
-        uint4 mv = ld_shared_v4(meta + uint32_t((tile * 128 + trow) * 16));
-        if (sc_align < 4) {
-          const uint32_t fifth = ld_shared_u32(meta + uint32_t(WT * 128 * 16 + (tile * 128 + trow) * 4));
-          const uint32_t row = uint32_t(it.e) * uint32_t(a.N) + uint32_t(it.n0 + min(tile * 128 + trow, a.N - 1 - it.n0));
-          const uint32_t sh = 8 * ((row * uint32_t(sc_stride) + uint32_t(c * sc_want)) & 3u);
-          mv.x = __funnelshift_r(mv.x, mv.y, sh);
-          mv.y = __funnelshift_r(mv.y, mv.z, sh);
-          mv.z = __funnelshift_r(mv.z, mv.w, sh);
-          mv.w = __funnelshift_r(mv.w, fifth, sh);
-        }
-        uint32_t zword = 0x88888888u;
-        if (FMT == GEMM_INT4) {
-          if (a.zeros) zword = ld_shared_u32(meta + uint32_t(WT * 128 * 20 + (tile * 128 + trow) * 4));
-          zword >>= 4 * ((c * (kExpChunk >> a.log2g)) & 7);  // the chunk's first group in the low nibble
-        }
-        for (int kb = 0; kb < nkb; ++kb, ++qk) {
-          if (WT == 1 && (qk & 1) != grp) continue;
-          uint32_t v[32];
-          const bool work = WT == 1 || tile < it.tiles;
-          if (work) {
-            uint32_t w[8];
+        uint32_t v[32];
+        if (kb < nkb) {
+          const uint32_t codes = sbase + uint32_t(s * S::CODE_BYTES + trow * 128);
+          uint32_t w[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 16-byte pieces of the row, at their 128B-swizzled places
-              const uint4 p = ld_shared_v4(codes + uint32_t(((2 * kb + h) ^ (trow & 7)) << 4));
-              w[4 * h] = p.x; w[4 * h + 1] = p.y; w[4 * h + 2] = p.z; w[4 * h + 3] = p.w;
+          for (int h = 0; h < 2; ++h) {  // 16-byte pieces of the row, at their 128B-swizzled places
+            const uint4 p = ld_shared_v4(codes + uint32_t(((2 * kb + h) ^ (trow & 7)) << 4));
+            w[4 * h] = p.x; w[4 * h + 1] = p.y; w[4 * h + 2] = p.z; w[4 * h + 3] = p.w;
+          }
+          uint4 mv = ld_shared_v4(meta + uint32_t(trow * 16));
+          if (sc_align < 4) {
+            const uint32_t fifth = ld_shared_u32(meta + uint32_t(128 * 16 + trow * 4));
+            const uint32_t row = uint32_t(it.e) * uint32_t(a.N) + uint32_t(it.n0 + min(trow, a.N - 1 - it.n0));
+            const uint32_t sh = 8 * ((row * uint32_t(sc_stride) + uint32_t(c * sc_want)) & 3u);
+            mv.x = __funnelshift_r(mv.x, mv.y, sh);
+            mv.y = __funnelshift_r(mv.y, mv.z, sh);
+            mv.z = __funnelshift_r(mv.z, mv.w, sh);
+            mv.w = __funnelshift_r(mv.w, fifth, sh);
+          }
+          if (FMT == GEMM_INT4) {
+            uint32_t zword = 0x88888888u;
+            if (a.zeros) zword = ld_shared_u32(meta + uint32_t(128 * 20 + trow * 4));
+            zword >>= 4 * ((c * (kExpChunk >> a.log2g)) & 7);  // the chunk's first group in the low nibble
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int g = (kb * 64 + h * 32) >> a.log2g;  // group within the chunk
+              const uint32_t word = g < 4 ? (g < 2 ? mv.x : mv.y) : (g < 6 ? mv.z : mv.w);
+              const float sc = __half2float(__ushort_as_half(uint16_t(g & 1 ? word >> 16 : word)));
+              const uint32_t hi = pack_bf16x2(sc, sc);
+              const float rest = sc - __uint_as_float(hi << 16);
+              const uint32_t lo = pack_bf16x2(rest, rest);
+              const uint32_t z128 = 0x43004300u + ((zword >> (4 * g)) & 15u) * 0x00010001u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], z128, hi, lo, v + 16 * h + 4 * j);
             }
-            const uint32_t m4[4] = {mv.x, mv.y, mv.z, mv.w};
-            if (FMT == GEMM_INT4) {
+          } else if (FMT == GEMM_NVFP4) {
+            const uint32_t sb = kb < 2 ? (kb == 0 ? mv.x : mv.y) : (kb == 2 ? mv.z : mv.w);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int g = (kb * 64 + h * 32) >> a.log2g;  // group within the chunk
-                const uint32_t word = g < 4 ? (g < 2 ? m4[0] : m4[1]) : (g < 6 ? m4[2] : m4[3]);
-                const float sc = __half2float(__ushort_as_half(uint16_t(g & 1 ? word >> 16 : word)));
-                const Int4Consts k = int4_consts(sc, float((zword >> (4 * g)) & 15u));
+            for (int h = 0; h < 2; ++h) {
+              uint32_t h2;
+              asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }"
+                  : "=r"(h2) : "r"((sb >> (16 * h)) & 0x7F7Fu));
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              // e2m1 2^-126 times sb 2^118: the epilogue multiplies by 2^8
+              const float lo = f.x * 0x1p118f, hi = f.y * 0x1p118f;
+              const uint32_t ml = pack_bf16x2(lo, lo), mh = pack_bf16x2(hi, hi);
+              dequant8_e2m1(w[4 * h], ml, v + 16 * h);
+              dequant8_e2m1(w[4 * h + 1], ml, v + 16 * h + 4);
+              dequant8_e2m1(w[4 * h + 2], mh, v + 16 * h + 8);
+              dequant8_e2m1(w[4 * h + 3], mh, v + 16 * h + 12);
+            }
+          } else {
+            const uint32_t sb = (kb < 2 ? mv.x : mv.y) >> (16 * (kb & 1));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], k, v + 16 * h + 4 * j);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t e8 = (sb >> (8 * h)) & 255u;
+              // {2^(e + 126), 2^(e + 126)} where bf16 holds it (e <= 1), else 2^126 and then 2^e
+              const bool large = __any_sync(0xffffffffu, e8 > 128u);
+              const uint32_t mul = large ? 0x7E807E80u : e8 * 0x00800080u + 0x3F003F00u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) dequant8_e2m1(w[4 * h + j], mul, v + 16 * h + 4 * j);
+              if (large) {
+                const uint32_t se = e8m0_bf16x2(e8);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[16 * h + j] = bf16x2_mul(v[16 * h + j], se);
               }
-            } else if (FMT == GEMM_NVFP4) {
-              const uint32_t sb = kb < 2 ? (kb == 0 ? m4[0] : m4[1]) : (kb == 2 ? m4[2] : m4[3]);
+            }
+            if (a.inv_s) {  // times 1/s in fp32, rounded to bf16 once
+              const int k0 = c * kExpChunk + kb * 64;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t h2;
-                asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h2) : "r"((sb >> (16 * h)) & 0x7F7Fu));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                // e2m1 2^-126 times sb 2^118: the epilogue multiplies by 2^8
-                const float lo = f.x * 0x1p118f, hi = f.y * 0x1p118f;
-                const uint32_t ml = pack_bf16x2(lo, lo), mh = pack_bf16x2(hi, hi);
-                dequant8_e2m1(w[4 * h], ml, v + 16 * h);
-                dequant8_e2m1(w[4 * h + 1], ml, v + 16 * h + 4);
-                dequant8_e2m1(w[4 * h + 2], mh, v + 16 * h + 8);
-                dequant8_e2m1(w[4 * h + 3], mh, v + 16 * h + 12);
-              }
-            } else {
-              const uint32_t sb = (kb < 2 ? m4[0] : m4[1]) >> (16 * (kb & 1));
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t e8 = (sb >> (8 * h)) & 255u;
-                // {2^(e + 126), 2^(e + 126)} where bf16 holds it (e <= 1), else 2^126 and then 2^e
-                const bool large = __any_sync(0xffffffffu, e8 > 128u);
-                const uint32_t mul = large ? 0x7E807E80u : e8 * 0x00800080u + 0x3F003F00u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) dequant8_e2m1(w[4 * h + j], mul, v + 16 * h + 4 * j);
-                if (large) {
-                  const uint32_t se = e8m0_bf16x2(e8);
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) v[16 * h + j] = bf16x2_mul(v[16 * h + j], se);
-                }
-              }
-              if (a.inv_s) {  // times 1/s in fp32, rounded to bf16 once
-                const int k0 = c * kExpChunk + kb * 64;
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                  if (k0 + 2 * j >= a.K) break;
-                  const float4 f = __ldg(reinterpret_cast<const float4*>(a.inv_s + k0 + 2 * j));
-                  v[j] = pack_bf16x2(__uint_as_float(v[j] << 16) * f.x, __uint_as_float(v[j] & 0xFFFF0000u) * f.y);
-                  v[j + 1] = pack_bf16x2(__uint_as_float(v[j + 1] << 16) * f.z, __uint_as_float(v[j + 1] & 0xFFFF0000u) * f.w);
-                }
+              for (int j = 0; j < 32; j += 2) {
+                if (k0 + 2 * j >= a.K) break;
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.inv_s + k0 + 2 * j));
+                v[j] = pack_bf16x2(__uint_as_float(v[j] << 16) * f.x, __uint_as_float(v[j] & 0xFFFF0000u) * f.y);
+                v[j + 1] = pack_bf16x2(__uint_as_float(v[j + 1] << 16) * f.z,
+                                       __uint_as_float(v[j + 1] & 0xFFFF0000u) * f.w);
               }
             }
           }
-          const int as = qk % AS, r = qk / AS;
-          if (r > 0 && !mbar_wait(&aempty[as], (r - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag)) ok = false;
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }  // tcgen05.st is warp-collective
-          if (work) {
-            tc_fence_after();
-            tmem_st32(tmem + lane_base + uint32_t(S::A_COL + (as * WT + tile) * 32), v);
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-          }
+          // the columns are free once the MMAs of this group's last k-block, four back, are done
+          const int qk = q + kb, p = qk - kExpGroups;
+          if (p >= 0) ok = mbar_wait(&mdone[p % XS], (p / XS) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);  // tcgen05.st is warp-collective
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st32(a_tmem, v);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&aready[as]);
+          if (lane == 0) mbar_arrive(&aready[grp]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[s]);
+        q += nkb;
+        if (++s == WS) {
+          s = 0;
+          wpar ^= 1u;
+        }
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + 4 * kExpGroups) {
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3;
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
@@ -538,52 +534,50 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       const int b = i % NACC, u = i / NACC;
       const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + it.e) * 256.0f : 1.0f;
-      bool go = mbar_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag);
+      const bool go = mbar_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag);
       if (!__all_sync(0xffffffffu, go)) break;
       tc_fence_after();
-      for (int t = 0; t < it.tiles; ++t) {
-        const int nw = it.n0 + t * 128 + quarter * 32;  // this warp's first weight row
-        for (int x = 0; x < it.rows; x += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_base + uint32_t(b * S::ACC_COLS + t * XT + x), v);
-          if (a.split > 1) {
-            // this CTA's part of the sums, fp32 [rows][128] over the rings (every copy and MMA
-            // of this only item is done)
-            float* part = reinterpret_cast<float*>(smem);
+      const int nw = it.n0 + quarter * 32;  // this warp's first weight row
+      for (int x = 0; x < it.rows; x += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_base + uint32_t(b * XT + x), v);
+        if (a.split > 1) {
+          // this CTA's part of the sums, fp32 [rows][128] over the rings (every copy and MMA
+          // of this only item is done)
+          float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (x + j < it.rows) part[(x + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]) * gmul;
+          continue;
+        }
+        if (!vec) {
+          const int n = nw + lane;
+          if (n < a.N) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (x + j < it.rows) part[(x + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]) * gmul;
-            continue;
+              if (x + j < it.rows) {
+                const float y = __uint_as_float(v[j]) * gmul;
+                a.Y[int64_t(it.row + x + j) * a.N + n] = uint16_t(pack_bf16x2(y, y));
+              }
           }
-          if (!vec) {
-            const int n = nw + lane;
-            if (n < a.N) {
+          continue;
+        }
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (x + j < it.rows) {
-                  const float y = __uint_as_float(v[j]) * gmul;
-                  a.Y[int64_t(it.row + x + j) * a.N + n] = uint16_t(pack_bf16x2(y, y));
-                }
-            }
-            continue;
+        for (int h = 0; h < 32; h += 16) {  // 16 rows of X: transpose, then 16-byte pieces of Y's rows
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const uint32_t y2 = pack_bf16x2(__uint_as_float(v[h + j]) * gmul, __uint_as_float(v[h + j + 1]) * gmul);
+            *reinterpret_cast<uint16_t*>(stage + j * 64 + lane * 2) = uint16_t(y2);
+            *reinterpret_cast<uint16_t*>(stage + (j + 1) * 64 + lane * 2) = uint16_t(y2 >> 16);
           }
+          __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 32; h += 16) {  // 16 rows of X: transpose, then 16-byte pieces of Y's rows
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const uint32_t y2 = pack_bf16x2(__uint_as_float(v[h + j]) * gmul, __uint_as_float(v[h + j + 1]) * gmul);
-              *reinterpret_cast<uint16_t*>(stage + j * 64 + lane * 2) = uint16_t(y2);
-              *reinterpret_cast<uint16_t*>(stage + (j + 1) * 64 + lane * 2) = uint16_t(y2 >> 16);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int p = 0; p < 16; p += 8) {
-              const int j = p + (lane >> 2), n = nw + (lane & 3) * 8;
-              if (x + h + j < it.rows && n < a.N)
-                *reinterpret_cast<uint4*>(a.Y + int64_t(it.row + x + h + j) * a.N + n) =
-                    *reinterpret_cast<const uint4*>(stage + j * 64 + (lane & 3) * 16);
-            }
+          for (int p = 0; p < 16; p += 8) {
+            const int j = p + (lane >> 2), n = nw + (lane & 3) * 8;
+            if (x + h + j < it.rows && n < a.N)
+              *reinterpret_cast<uint4*>(a.Y + int64_t(it.row + x + h + j) * a.N + n) =
+                  *reinterpret_cast<const uint4*>(stage + j * 64 + (lane & 3) * 16);
           }
         }
       }

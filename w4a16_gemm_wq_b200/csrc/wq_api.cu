@@ -615,11 +615,9 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   // the host does not know how the rows fall on the experts: at most min(E, T) hold any, and
   // each adds at most one partly filled tile
   const int64_t holders = std::min(a.E, a.T);
-  const auto items = [&](int wt, int xt) {
-    return (holders + a.T / xt) * ((int64_t(a.N) + 128 * wt - 1) / (128 * wt));
-  };
-  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(2, 192), st);
-  const int64_t n = items(1, 64);
+  const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
+  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(192), st);
+  const int64_t n = items(64);
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
   const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
   return launch_expert_shape<FMT, wq::ExpNarrow>(a, X, packed, split, n, st);
