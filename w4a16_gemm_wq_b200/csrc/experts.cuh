@@ -14,14 +14,16 @@
 // shared memory.
 //
 // One CTA walks items (expert, row tile, 128 weight rows).  Roles:
-//   warp 0       codes [128 x 256 k] by TMA, with the rows' scales and zero points
-//                by cp.async, into a ring of WS stages
-//   warp 1       X boxes [XBOX rows x 64 k] by TMA into a ring of XS slots
+//   warp 0       codes [128 x 256 k] by TMA into a ring of WS stages
+//   warp 1       X boxes [XBOX rows x 64 k] by TMA into a ring of XS slots of SK
+//                k-blocks (64 k) each
 //   warp 2       TMEM allocation and the MMA issuer (a whole warp in step, one
 //                elected lane issues: a lone lane's branch costs 46 clocks an
 //                instruction against 9 measured here)
+//   warp 3       the experts' row tiles, then the scales and zero points of the
+//                codes' rows by cp.async into the stages of the codes
 //   warps 4-19   dequantizers: four groups of four warps, one 64-wide k-block of
-//                every four each, into its own 32 columns of tensor memory
+//                every chunk of 256 k each, into 32 columns of tensor memory
 //   warps 20-23  epilogue: tcgen05.ld, transpose in shared memory, store Y
 // All waits are bounded; see mbar_wait.
 #pragma once
@@ -53,34 +55,37 @@ struct ExpertArgs {
   int split;               // CTAs of a cluster that share an item along K (1: none)
 };
 
-constexpr int kExpGroups = 4;      // dequantizer groups, and stages of dequantized weights (32 columns each)
+constexpr int kExpGroups = 4;      // dequantizer groups: one k-block of a chunk each
 
 // Up to XT rows of X per item, in boxes of XBOX; NACC accumulators (2: the
-// epilogue overlaps the next item); WS stages of codes, XS slots of X.
-template <int XT_, int XBOX_, int NACC_, int WS_, int XS_>
+// epilogue overlaps the next item); WS stages of codes.  X slots and stages of
+// dequantized weights hold SK k-blocks each: one pair of waits and one commit of the
+// MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.
+template <int XT_, int XBOX_, int NACC_, int WS_, int XS_, int SK_>
 struct ExpShape {
-  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_;
+  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_;
+  static constexpr int AS = SK == 1 ? 4 : 2;  // stages of dequantized weights, 32 SK columns each
   static constexpr int CODE_BYTES = 128 * 128;
   static constexpr int META_BYTES = 128 * 24;  // per row 16 bytes of scales, a fifth word, a word of zero points
-  static constexpr int SLOT_BYTES = XT * 128;
+  static constexpr int SLOT_BYTES = SK * XT * 128;
   static constexpr int OFF_X = WS * CODE_BYTES;
   static constexpr int OFF_META = OFF_X + XS * SLOT_BYTES;
   static constexpr int OFF_STAGE = OFF_META + WS * META_BYTES;
   static constexpr int OFF_TAB = OFF_STAGE + 4 * 1024;
   static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxExperts + 4) * 4;
-  static constexpr int NBAR = 2 * WS + 2 * XS + kExpGroups + 2 * NACC;
+  static constexpr int NBAR = 2 * WS + 2 * XS + AS + 2 * NACC;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr int A_COL = NACC * XT;
-  static constexpr int USED_COLS = A_COL + kExpGroups * 32;
+  static constexpr int USED_COLS = A_COL + AS * SK * 32;
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static_assert(USED_COLS <= 512, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(XT % 16 == 0 && XT <= 256 && XT % XBOX == 0 && XBOX % 8 == 0, "row tiles");
-  static_assert(XS >= kExpGroups, "a dequantizer waits for the k-block four back on the slots' barriers");
+  static_assert(4 % SK == 0 && XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
-using ExpWide = ExpShape<192, 32, 2, 4, 5>;
-using ExpNarrow = ExpShape<64, 8, 2, 6, 8>;
+using ExpWide = ExpShape<192, 32, 2, 3, 3, 2>;
+using ExpNarrow = ExpShape<64, 8, 2, 5, 3, 4>;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -169,7 +174,7 @@ __device__ __forceinline__ void dequant8_e2m1(uint32_t w, uint32_t mul2, uint32_
 
 template <int FMT, typename S>
 __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertArgs a) {
-  constexpr int XT = S::XT, WS = S::WS, XS = S::XS, NACC = S::NACC;
+  constexpr int XT = S::XT, WS = S::WS, XS = S::XS, NACC = S::NACC, SK = S::SK, AS = S::AS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
@@ -181,75 +186,80 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   uint64_t* xfull = wempty + WS;          // X boxes landed
   uint64_t* mdone = xfull + XS;           // MMAs of the k-block in this slot finished
   uint64_t* aready = mdone + XS;          // dequantized weights in tensor memory
-  uint64_t* dfull = aready + kExpGroups;  // accumulator complete
+  uint64_t* dfull = aready + AS;          // accumulator complete
   uint64_t* dempty = dfull + NACC;        // accumulator drained
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + NACC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* scan = reinterpret_cast<int*>(smem + S::OFF_STAGE);  // [24], before the epilogue uses it
+  int* bad_flag = reinterpret_cast<int*>(tmem_slot + 2);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (threadIdx.x < S::NBAR) {
-    // arrivals: codes = the TMA's thread and the 32 lanes that copy the scales; one arrival a warp elsewhere
-    const int b = threadIdx.x;
-    mbar_init(&bars[b], b < WS ? 33 : b < 2 * WS ? 4 * kExpGroups : b < 2 * (WS + XS) ? 1
-                        : b < 2 * (WS + XS) + kExpGroups ? 4 : b < 2 * (WS + XS) + kExpGroups + NACC ? 1 : 4);
+  if (warp == 0) {
+    for (int b = lane; b < S::NBAR; b += 32)
+      // arrivals: codes = the TMA's thread and the 32 lanes that copy the scales; one arrival a warp elsewhere
+      mbar_init(&bars[b], b < WS ? 33 : b < 2 * WS ? 4 * kExpGroups : b < 2 * (WS + XS) ? 1
+                          : b < 2 * (WS + XS) + AS ? 4 * SK : b < 2 * (WS + XS) + AS + NACC ? 1 : 4);
     fence_mbar_init();
-  }
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    prefetch_tmap(&a.tmW);
-    prefetch_tmap(&a.tmX);
-  }
-  if (warp == 2) {
+    if (lane == 0) {
+      *abort_flag = 0;
+      prefetch_tmap(&a.tmW);
+      prefetch_tmap(&a.tmX);
+    }
+  } else if (warp == 2) {
     tmem_alloc(tmem_slot, S::TMEM_COLS);
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // ---- row bounds and first row tiles of the experts (two experts per thread)
-  bool bad = false;
-  {
-    const int e0 = 2 * threadIdx.x;
-    int b[3] = {0, 0, 0}, t[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (e0 + j <= a.E) b[j] = a.offsets ? __ldg(a.offsets + e0 + j) : (e0 + j ? a.T : 0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (e0 + j < a.E) {
-        bad |= b[j] < 0 || b[j + 1] < b[j] || b[j + 1] > a.T;
-        t[j] = bad ? 0 : (b[j + 1] - b[j] + XT - 1) / XT;
-      }
-    int inc = t[0] + t[1];
+  if (warp == 3) {
+    // row bounds and first row tiles of the experts: each lane takes `per` of them in a row
+    const int per = (a.E + 31) >> 5, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
+    const auto bound_of = [&](int e) { return a.offsets ? __ldg(a.offsets + e) : (e ? a.T : 0); };
+    bool bad = false;
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+      const int b0 = bound_of(e), b1 = bound_of(e + 1);
+      bad |= b0 < 0 || b1 < b0 || b1 > a.T;
+      sum += (b1 - b0 + XT - 1) / XT;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    int t = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += v;
+      const int v = __shfl_up_sync(0xffffffffu, t, off);
+      if (lane >= off) t += v;
     }
-    if (lane == 31) scan[warp] = inc;
-    tc_fence_before();
-    bad = __syncthreads_or(bad);
-    tc_fence_after();
-    int before = inc - t[0] - t[1];
-    for (int w = 0; w < warp; ++w) before += scan[w];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (e0 + j <= a.E) {
-        bound[e0 + j] = b[j];
-        tstart[e0 + j] = before;
-        before += t[j];
+    t -= sum;
+    for (int e = e0; e < e1; ++e) {
+      const int b0 = bound_of(e), b1 = bound_of(e + 1);
+      bound[e] = b0;
+      tstart[e] = t;
+      t += (b1 - b0 + XT - 1) / XT;
+      if (e == a.E - 1) {
+        bound[a.E] = b1;
+        tstart[a.E] = t;
       }
-    __syncthreads();
+    }
+    if (lane == 0) {
+      *bad_flag = bad;
+      if (bad && blockIdx.x == 0) report_error(ERR_OFFSETS);
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (bad && threadIdx.x == 0 && blockIdx.x == 0) report_error(ERR_OFFSETS);
   const int nblocks = (a.N + 127) >> 7;
-  const int items = bad ? 0 : tstart[a.E] * nblocks;
+  const int items = *bad_flag ? 0 : tstart[a.E] * nblocks;
   const int nchunks = (a.K + kExpChunk - 1) / kExpChunk;
-  const int rank = a.split > 1 ? int(cluster_ctarank()) : 0;
-  const int c0 = nchunks * rank / a.split, c1 = nchunks * (rank + 1) / a.split;  // this CTA's chunks of an item
-  const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
+  // this CTA's items, and its chunks of an item
+  int rank = 0, c0 = 0, c1 = nchunks, first = blockIdx.x, step = gridDim.x;
+  if (a.split > 1) {
+    rank = int(cluster_ctarank());
+    c0 = nchunks * rank / a.split;
+    c1 = nchunks * (rank + 1) / a.split;
+    first /= a.split;
+    step /= a.split;
+  }
 
   struct Item {
     int e, row, rows, n0;  // expert, first row of X and their number, first weight row
@@ -270,7 +280,8 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     it.rows = min(w, bound[lo + 1] - it.row);
     return it;
   };
-  const auto kblocks_of = [&](int c) { return min(4, (a.K - c * kExpChunk + 63) >> 6); };
+  // stages of a chunk: whole ones, the k-blocks past K are zeros (of the codes, the scales and X)
+  const auto stages_of = [&](int c) { return min(4 / SK, (a.K - c * kExpChunk + 64 * SK - 1) / (64 * SK)); };
   // a row's scale bytes, those of a chunk, and the largest alignment that all chunks of all rows share
   const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
   const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
@@ -278,78 +289,109 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   const int sc_align = (sc_stride | sc_want) & -(sc_stride | sc_want);
 
   if (warp == 0) {
-    // ---------------------------------------------------------- codes and scales
-    int q = 0;
+    // ---------------------------------------------------------- codes
+    int q = 0, s = 0;
+    uint32_t par = 1;  // parity of the stage's last use (the first use waits for none)
     bool ok = true;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
-      const int64_t row0 = int64_t(it.e) * a.N + it.n0;
+      const int row0 = it.e * a.N + it.n0;
       for (int c = c0; c < c1; ++c, ++q) {
-        const int s = q % WS, r = q / WS;
-        if (r > 0) ok = mbar_wait(&wempty[s], (r - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+        if (q >= WS) ok = mbar_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&wfull[s], uint32_t(S::CODE_BYTES));
-          tma_load_2d(smem + s * S::CODE_BYTES, &a.tmW, &wfull[s], c * 128, int(row0));
+          tma_load_2d(smem + s * S::CODE_BYTES, &a.tmW, &wfull[s], c * 128, row0);
         }
         __syncwarp();
-        const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
-#pragma unroll 1
-        for (int t = lane; t < 128; t += 32) {
-          const int64_t row = row0 + min(t, a.N - 1 - it.n0);
-          // the row's scale bytes of this chunk; those past the row's end arrive as zeros
-          const uint8_t* src = sc_base + row * sc_stride + int64_t(c) * sc_want;
-          const int have = min(sc_want, sc_stride - c * sc_want);
-          const uint32_t dst = meta + uint32_t(t) * 16u;
-          if (sc_align == 16) {
-            cp_async_zfill<16>(dst, src, uint32_t(have));
-          } else if (sc_align == 8) {
-            for (int b = 0; b < sc_want; b += 8)
-              cp_async_zfill<8>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(8, have - b))));
-          } else if (sc_align == 4) {
-            for (int b = 0; b < sc_want; b += 4)
-              cp_async_zfill<4>(dst + b, src + (b < have ? b : 0), uint32_t(max(0, min(4, have - b))));
-          } else {
-            // rows that start inside a word: the words around the bytes, which the dequantizer shifts
-            const int off = int(reinterpret_cast<uintptr_t>(src) & 3);
-            for (int b = 0; b <= sc_want; b += 4) {
-              const int n = max(0, min(4, off + have - b));
-              cp_async_zfill<4>(b < 16 ? dst + b : meta + uint32_t(128 * 16 + t * 4), src - off + (n ? b : 0),
-                                uint32_t(n));
-            }
-          }
-          if (FMT == GEMM_INT4 && a.zeros) {
-            const int ng = a.K >> a.log2g, zw = (ng + 7) >> 3;
-            const int word = (c * (kExpChunk >> a.log2g)) >> 3;
-            cp_async_zfill<4>(meta + uint32_t(128 * 20 + t * 4), a.zeros + row * zw + word, 4);
-          }
+        if (++s == WS) {
+          s = 0;
+          par ^= 1u;
         }
-        cp_async_arrive(&wfull[s]);
       }
     }
     if (!ok) {  // let copies already issued land before the CTA leaves
       for (int k = (q > WS ? q - WS : 0); k < q; ++k) mbar_wait(&wfull[k % WS], (k / WS) & 1, ERR_TIMEOUT_TMA, nullptr);
     }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------- scales and zero points
+    int q = 0, s = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    const int zw = ((a.K >> a.log2g) + 7) >> 3;
+    for (int id = first; id < items && ok; id += step) {
+      const Item it = item_of(id);
+      const uint8_t* src[4];  // this lane's four rows: lane, lane + 32, ..
+      const uint32_t* zsrc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int64_t row = int64_t(it.e) * a.N + min(it.n0 + lane + 32 * t, a.N - 1);
+        src[t] = sc_base + row * sc_stride;
+        zsrc[t] = a.zeros + row * zw;
+      }
+      for (int c = c0; c < c1; ++c, ++q) {
+        if (q >= WS) ok = mbar_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES) + uint32_t(lane * 16);
+        const int at = c * sc_want, have = sc_stride - at;  // bytes past the row's end arrive as zeros
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t dst = meta + uint32_t(t * 512);
+          const uint8_t* p = src[t] + at;
+          if (sc_align == 16) {
+            cp_async_zfill<16>(dst, p, uint32_t(min(16, have)));
+          } else if (sc_align == 8) {
+            cp_async_zfill<8>(dst, p, uint32_t(min(8, have)));
+            if (sc_want == 16) cp_async_zfill<8>(dst + 8, have > 8 ? p + 8 : p, uint32_t(max(0, min(8, have - 8))));
+          } else if (sc_align == 4) {
+#pragma unroll 1
+            for (int b = 0; b < sc_want; b += 4)
+              cp_async_zfill<4>(dst + b, b < have ? p + b : p, uint32_t(max(0, min(4, have - b))));
+          } else {
+            // rows that start inside a word: the words around the bytes, which the dequantizer shifts
+            const int off = int(reinterpret_cast<uintptr_t>(p) & 3), end = off + min(sc_want, have);
+#pragma unroll 1
+            for (int b = 0; b <= sc_want; b += 4) {
+              const int n = max(0, min(4, end - b));
+              cp_async_zfill<4>(b < 16 ? dst + b : meta + uint32_t(128 * 16 + t * 128) - uint32_t(lane * 12),
+                                p - off + (n ? b : 0), uint32_t(n));
+            }
+          }
+          if (FMT == GEMM_INT4 && a.zeros)
+            cp_async_zfill<4>(meta + uint32_t(128 * 20 + t * 128) - uint32_t(lane * 12),
+                              zsrc[t] + ((c * (kExpChunk >> a.log2g)) >> 3), 4);
+        }
+        cp_async_arrive(&wfull[s]);
+        if (++s == WS) {
+          s = 0;
+          par ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ---------------------------------------------------------- rows of X
     int q = 0, s = 0;
-    uint32_t par = 1;  // parity of the slot's last use (the first use waits for none)
+    uint32_t par = 1;
     bool ok = true;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
       const int boxes = (it.rows + S::XBOX - 1) / S::XBOX;
       for (int c = c0; c < c1 && ok; ++c) {
-        const int nkb = kblocks_of(c);
-        for (int kb = 0; kb < nkb; ++kb, ++q) {
+        const int nst = stages_of(c);
+        for (int h = 0; h < nst; ++h, ++q) {
           if (q >= XS) ok = mbar_wait(&mdone[s], par, ERR_TIMEOUT_PIPE, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&xfull[s], uint32_t(boxes * S::XBOX) * 128u);
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d(smem + S::OFF_X + s * S::SLOT_BYTES + b * S::XBOX * 128, &a.tmX, &xfull[s],
-                          c * kExpChunk + kb * 64, it.row + b * S::XBOX);
+            mbar_arrive_expect_tx(&xfull[s], uint32_t(SK * boxes * S::XBOX) * 128u);
+#pragma unroll
+            for (int j = 0; j < SK; ++j)
+              for (int b = 0; b < boxes; ++b)
+                tma_load_2d(smem + S::OFF_X + s * S::SLOT_BYTES + j * XT * 128 + b * S::XBOX * 128, &a.tmX, &xfull[s],
+                            c * kExpChunk + (h * SK + j) * 64, it.row + b * S::XBOX);
           }
           __syncwarp();
           if (++s == XS) {
@@ -364,9 +406,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- MMA issuer
-    int q = 0, i = 0, xs = 0;
-    uint32_t xpar = 0;
+    int q = 0, i = 0, xs = 0, as = 0;
+    uint32_t xpar = 0, apar = 0;
     bool ok = true;
+    const uint64_t xd0 = desc_kmajor_sw128(sbase + uint32_t(S::OFF_X));
     for (int id = first; id < items && ok; id += step, ++i) {
       const Item it = item_of(id);
       const uint32_t idesc = idesc_bf16_f32(128, (it.rows + 15) & ~15);
@@ -374,24 +417,24 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       if (u > 0) ok = mbar_wait(&dempty[b], (u - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      tc_fence_after();
       const uint32_t acc = tmem + uint32_t(b * XT);
       uint32_t more = 0;
       for (int c = c0; c < c1 && ok; ++c) {
-        const int nkb = kblocks_of(c);
-        for (int kb = 0; kb < nkb; ++kb, ++q) {
-          const int as = q % kExpGroups;
-          ok = mbar_wait(&xfull[xs], xpar, ERR_TIMEOUT_TMA, abort_flag) &&
-               mbar_wait(&aready[as], (q / kExpGroups) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+        const int nst = stages_of(c);
+        for (int h = 0; h < nst; ++h, ++q) {
+          const bool xr = mbar_try_wait(&xfull[xs], xpar), ar = mbar_try_wait(&aready[as], apar);
+          ok = (xr || mbar_wait(&xfull[xs], xpar, ERR_TIMEOUT_TMA, abort_flag)) &&
+               (ar || mbar_wait(&aready[as], apar, ERR_TIMEOUT_PIPE, abort_flag));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t xd = desc_kmajor_sw128(sbase + uint32_t(S::OFF_X + xs * S::SLOT_BYTES));
-          const uint32_t at = tmem + uint32_t(S::A_COL + as * 32);
           if (elect_one()) {
+            const uint64_t xd = xd0 + uint64_t(uint32_t(xs * (S::SLOT_BYTES >> 4)));
+            const uint32_t at = tmem + uint32_t(S::A_COL + as * SK * 32);
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)  // K = 16: 8 columns of A, 32 bytes inside X's swizzle atom
-              umma_bf16_ts(acc, at + uint32_t(8 * k4), xd + uint64_t(2 * k4), idesc, more | uint32_t(k4));
+            for (int k = 0; k < 4 * SK; ++k)  // K = 16: 8 columns of A, 32 bytes inside X's swizzle atom
+              umma_bf16_ts(acc, at + uint32_t(8 * k), xd + uint64_t((k >> 2) * (XT * 8) + 2 * (k & 3)), idesc,
+                           more | uint32_t(k));
             umma_commit(&mdone[xs]);
           }
           __syncwarp();
@@ -400,6 +443,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
             xs = 0;
             xpar ^= 1u;
           }
+          if (++as == AS) {
+            as = 0;
+            apar ^= 1u;
+          }
         }
       }
       if (elect_one()) umma_commit(&dfull[b]);  // also after an abort: completes when the issued MMAs are done
@@ -407,24 +454,23 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     }
   } else if (warp >= 4 && warp < 4 + 4 * kExpGroups) {
     // ---------------------------------------------------------- dequantizers
-    const int grp = (warp - 4) >> 2;       // takes the k-blocks q with q % 4 == grp
+    const int kb = (warp - 4) >> 2;        // this group's k-block of every chunk
     const int quarter = warp & 3;          // TMEM lanes of this warp
     const int trow = quarter * 32 + lane;  // weight row within the tile
-    const uint32_t a_tmem = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(S::A_COL + grp * 32);
-    int s = 0, q = 0;
+    const uint32_t a_tmem = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(S::A_COL + (kb % SK) * 32);
+    int s = 0, q = 0;  // stage of the codes; stages of dequantized weights before this chunk
     uint32_t wpar = 0;
     bool ok = true;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
       for (int c = c0; c < c1; ++c) {
-        const int nkb = kblocks_of(c);
+        const int nst = stages_of(c);
         ok = mbar_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int kb = (grp - q) & (kExpGroups - 1);  // this group's k-block of the chunk
         const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
         uint32_t v[32];
-        if (kb < nkb) {
+        if (kb < nst * SK) {
           const uint32_t codes = sbase + uint32_t(s * S::CODE_BYTES + trow * 128);
           uint32_t w[8];
 #pragma unroll
@@ -502,21 +548,21 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
               }
             }
           }
-          // the columns are free once the MMAs of this group's last k-block, four back, are done
-          const int qk = q + kb, p = qk - kExpGroups;
+          // the columns are free once the MMAs of the stage AS back are done
+          const int n = q + kb / SK, p = n - AS, as = n % AS;
           if (p >= 0) ok = mbar_wait(&mdone[p % XS], (p / XS) & 1, ERR_TIMEOUT_PIPE, abort_flag);
           ok = __all_sync(0xffffffffu, ok);  // tcgen05.st is warp-collective
           if (!ok) break;
           tc_fence_after();
-          tmem_st32(a_tmem, v);
+          tmem_st32(a_tmem + uint32_t(as * SK * 32), v);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&aready[grp]);
+          if (lane == 0) mbar_arrive(&aready[as]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[s]);
-        q += nkb;
+        q += nst;
         if (++s == WS) {
           s = 0;
           wpar ^= 1u;
