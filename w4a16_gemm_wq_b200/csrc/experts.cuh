@@ -125,11 +125,6 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
 // One lane of a converged warp: the compiler then knows the branch's warp to be in step.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -137,39 +132,69 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The integer pipe that shifts, masks and permutes runs at half the rate of the
-// multiply-add pipe, and bounds the dequantization: both forms below move what they
-// can to multiply-adds.
-//
-// INT4: (q - z) s of the 8 codes of a word in natural order.  d = (128 + q) - (128 + z)
-// is exact in bf16; the fp16 scale is the exact sum of two bf16, s = hi + lo, and
-// fma(d, hi, d lo) rounds to bf16 once (d lo's own rounding is 2^-9 of 2^-9 of the
-// value).
-__device__ __forceinline__ void dequant8_int4(uint32_t w, uint32_t z128, uint32_t hi, uint32_t lo, uint32_t* out) {
-  uint32_t p[4];  // {code i, code i + 4}
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t d = bf16x2_sub(lop3_andor(w >> (4 * i), 0x000F000Fu, 0x43004300u), z128);
-    p[i] = bf16x2_fma(d, hi, bf16x2_mul(d, lo));
-  }
-  out[0] = prmt_b32(p[0], p[1], 0x5410);
-  out[1] = prmt_b32(p[2], p[3], 0x5410);
-  out[2] = prmt_b32(p[0], p[1], 0x7632);
-  out[3] = prmt_b32(p[2], p[3], 0x7632);
+// d = a * b + c with fp16 a (half `hi_a` of a pair) and b, fp32 c and d.
+template <int HI_A, int HI_B>
+__device__ __forceinline__ float fma_f16_f32(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("{ .reg .b16 a0, a1, b0, b1;\n\t mov.b32 {a0, a1}, %1;\n\t mov.b32 {b0, b1}, %2;\n\t"
+      "fma.rn.f32.f16 %0, a%4, b%5, %3; }"
+      : "=f"(d)
+      : "r"(a), "r"(b), "f"(c), "n"(HI_A), "n"(HI_B));
+  return d;
 }
 
-// E2M1: the 8 codes of a word as bf16 pairs e2m1 2^-126 in natural order, times
-// mul2 = {m, m} (exact: at most 6 significant bits).  A code's sign at bit 15 and its
-// three low bits at bits 8-6 are that bf16 (0.5 is its subnormal): the code times 64
-// puts the low bits there and the sign at bit 9, and sign (4096 - 64) moves it to bit 15.
-__device__ __forceinline__ void dequant8_e2m1(uint32_t w, uint32_t mul2, uint32_t* out) {
-  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+// Dequantization is bound by the integer pipe (shifts, masks, permutes and the
+// conversions), which takes an instruction of a warp every second clock, as the
+// multiply-add pipe does for packed and integer products but not for fp32 ones with
+// fp16 factors (every clock).  Measured on the alternatives: 5 clocks a pair of INT4
+// codes and 4.3 of E2M1 codes in this form, 6 each with packed bf16 arithmetic.
+//
+// INT4: 16 (q - z) s of the 8 codes of a word in natural order, rounded to bf16 once:
+// a code at bits 4-7 under the exponent of 1024 is the fp16 value 1024 + 16 q, and one
+// multiply-add by the fp16 scale with c = -16 (64 + z) s (exact: 7 by 11 bits) gives
+// 16 (q - z) s exactly in fp32.  The epilogue divides by 16.
+__device__ __forceinline__ void dequant8_int4(uint32_t w, uint32_t s, float c, uint32_t* out) {
+  constexpr uint32_t M = 0x00F000F0u, B = 0x64006400u;
+  const uint32_t p0 = lop3_andor(w * 16u, M, B), p1 = lop3_andor(w, M, B);  // {code i, code i + 4}
+  const uint32_t p2 = lop3_andor(w >> 4, M, B), p3 = lop3_andor(w >> 8, M, B);
+  out[0] = pack_bf16x2(fma_f16_f32<0, 0>(p0, s, c), fma_f16_f32<0, 0>(p1, s, c));
+  out[1] = pack_bf16x2(fma_f16_f32<0, 0>(p2, s, c), fma_f16_f32<0, 0>(p3, s, c));
+  out[2] = pack_bf16x2(fma_f16_f32<1, 0>(p0, s, c), fma_f16_f32<1, 0>(p1, s, c));
+  out[3] = pack_bf16x2(fma_f16_f32<1, 0>(p2, s, c), fma_f16_f32<1, 0>(p3, s, c));
+}
+
+// Byte B of w: two E2M1 codes as fp16 values, the first in the low half.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_of_byte(uint32_t w) {
+  uint32_t h;
+  asm("{ .reg .b8 q0, q1, q2, q3;\n\t mov.b32 {q0, q1, q2, q3}, %1;\n\t cvt.rn.f16x2.e2m1x2 %0, q%2; }"
+      : "=r"(h) : "r"(w), "n"(B));
+  return h;
+}
+// E2M1: the 8 codes of a word times the fp16 scale in half HI of s, as bf16 pairs (exact).
+template <int HI>
+__device__ __forceinline__ void dequant8_e2m1(uint32_t w, uint32_t s, uint32_t* out) {
+  const uint32_t h[4] = {e2m1x2_of_byte<0>(w), e2m1x2_of_byte<1>(w), e2m1x2_of_byte<2>(w), e2m1x2_of_byte<3>(w)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = pack_bf16x2(fma_f16_f32<0, HI>(h[i], s, 0.f), fma_f16_f32<1, HI>(h[i], s, 0.f));
+}
+// The same times an fp32 scale and, where given, fp32 factors f[0..7] (rounded to bf16 once).
+__device__ __forceinline__ void dequant8_e2m1_f32(uint32_t w, float s, const float* __restrict__ f, uint32_t* out) {
+  const uint32_t h[4] = {e2m1x2_of_byte<0>(w), e2m1x2_of_byte<1>(w), e2m1x2_of_byte<2>(w), e2m1x2_of_byte<3>(w)};
+  float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // {code 2i, code 2i + 1}, zero-extended: a selector with bit 3 set replicates the byte's top bit, which is 0
-    const uint32_t r = prmt_b32(even, odd, uint32_t(i | ((i | 8) << 4) | ((4 + i) << 8) | ((4 + i + 8) << 12)));
-    out[i] = bf16x2_mul(r * 64u + (r & 0x00080008u) * 4032u, mul2);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    x[2 * i] = v.x * s;
+    x[2 * i + 1] = v.y * s;
   }
+  if (f) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(f)), b = __ldg(reinterpret_cast<const float4*>(f) + 1);
+    x[0] *= a.x; x[1] *= a.y; x[2] *= a.z; x[3] *= a.w;
+    x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
 }
 
 template <int FMT, typename S>
@@ -496,55 +521,40 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
             for (int h = 0; h < 2; ++h) {
               const int g = (kb * 64 + h * 32) >> a.log2g;  // group within the chunk
               const uint32_t word = g < 4 ? (g < 2 ? mv.x : mv.y) : (g < 6 ? mv.z : mv.w);
-              const float sc = __half2float(__ushort_as_half(uint16_t(g & 1 ? word >> 16 : word)));
-              const uint32_t hi = pack_bf16x2(sc, sc);
-              const float rest = sc - __uint_as_float(hi << 16);
-              const uint32_t lo = pack_bf16x2(rest, rest);
-              const uint32_t z128 = 0x43004300u + ((zword >> (4 * g)) & 15u) * 0x00010001u;
+              const uint32_t sc = g & 1 ? word >> 16 : word;
+              const float z = float((zword >> (4 * g)) & 15u);
+              const float cz = -16.f * (64.f + z) * __half2float(__ushort_as_half(uint16_t(sc)));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], z128, hi, lo, v + 16 * h + 4 * j);
+              for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], sc, cz, v + 16 * h + 4 * j);
             }
           } else if (FMT == GEMM_NVFP4) {
             const uint32_t sb = kb < 2 ? (kb == 0 ? mv.x : mv.y) : (kb == 2 ? mv.z : mv.w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint32_t h2;
+              uint32_t s2;  // the scales of the two blocks, fp16 (exact)
               asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }"
-                  : "=r"(h2) : "r"((sb >> (16 * h)) & 0x7F7Fu));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              // e2m1 2^-126 times sb 2^118: the epilogue multiplies by 2^8
-              const float lo = f.x * 0x1p118f, hi = f.y * 0x1p118f;
-              const uint32_t ml = pack_bf16x2(lo, lo), mh = pack_bf16x2(hi, hi);
-              dequant8_e2m1(w[4 * h], ml, v + 16 * h);
-              dequant8_e2m1(w[4 * h + 1], ml, v + 16 * h + 4);
-              dequant8_e2m1(w[4 * h + 2], mh, v + 16 * h + 8);
-              dequant8_e2m1(w[4 * h + 3], mh, v + 16 * h + 12);
+                  : "=r"(s2) : "r"((sb >> (16 * h)) & 0x7F7Fu));
+              dequant8_e2m1<0>(w[4 * h], s2, v + 16 * h);
+              dequant8_e2m1<0>(w[4 * h + 1], s2, v + 16 * h + 4);
+              dequant8_e2m1<1>(w[4 * h + 2], s2, v + 16 * h + 8);
+              dequant8_e2m1<1>(w[4 * h + 3], s2, v + 16 * h + 12);
             }
           } else {
             const uint32_t sb = (kb < 2 ? mv.x : mv.y) >> (16 * (kb & 1));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t e8 = (sb >> (8 * h)) & 255u;
-              // {2^(e + 126), 2^(e + 126)} where bf16 holds it (e <= 1), else 2^126 and then 2^e
-              const bool large = __any_sync(0xffffffffu, e8 > 128u);
-              const uint32_t mul = large ? 0x7E807E80u : e8 * 0x00800080u + 0x3F003F00u;
+              // a scale that is a normal fp16 (2^-14 .. 2^15) for the whole warp, or fp32 products
+              if (!a.inv_s && __all_sync(0xffffffffu, e8 - 113u < 30u)) {
+                const uint32_t s2 = (e8 - 112u) << 10;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) dequant8_e2m1(w[4 * h + j], mul, v + 16 * h + 4 * j);
-              if (large) {
-                const uint32_t se = e8m0_bf16x2(e8);
+                for (int j = 0; j < 4; ++j) dequant8_e2m1<0>(w[4 * h + j], s2, v + 16 * h + 4 * j);
+              } else {
+                const int k0 = c * kExpChunk + kb * 64 + h * 32;
+                const float* f = a.inv_s && k0 < a.K ? a.inv_s + k0 : nullptr;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[16 * h + j] = bf16x2_mul(v[16 * h + j], se);
-              }
-            }
-            if (a.inv_s) {  // times 1/s in fp32, rounded to bf16 once
-              const int k0 = c * kExpChunk + kb * 64;
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                if (k0 + 2 * j >= a.K) break;
-                const float4 f = __ldg(reinterpret_cast<const float4*>(a.inv_s + k0 + 2 * j));
-                v[j] = pack_bf16x2(__uint_as_float(v[j] << 16) * f.x, __uint_as_float(v[j] & 0xFFFF0000u) * f.y);
-                v[j + 1] = pack_bf16x2(__uint_as_float(v[j + 1] << 16) * f.z,
-                                       __uint_as_float(v[j + 1] & 0xFFFF0000u) * f.w);
+                for (int j = 0; j < 4; ++j)
+                  dequant8_e2m1_f32(w[4 * h + j], e8m0_f32(e8), f ? f + 8 * j : nullptr, v + 16 * h + 4 * j);
               }
             }
           }
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     for (int id = first; id < items; id += step, ++i) {
       const Item it = item_of(id);
       const int b = i % NACC, u = i / NACC;
-      const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + it.e) * 256.0f : 1.0f;
+      const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + it.e) : FMT == GEMM_INT4 ? 0.0625f : 1.0f;
       const bool go = mbar_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag);
       if (!__all_sync(0xffffffffu, go)) break;
       tc_fence_after();
