@@ -25,7 +25,7 @@
 //   warps 4-19   dequantizers: four groups of four warps, one 64-wide k-block of
 //                every chunk of 256 k each, into 32 columns of tensor memory
 //   warps 20-23  epilogue: tcgen05.ld, transpose in shared memory, store Y
-// All waits are bounded; see mbar_wait.
+// All waits are bounded; see warp_wait.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -106,6 +106,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
+}
+
+// mbar_wait for a converged warp, with one answer for all its lanes: true once the
+// phase of the given parity is complete, false on a timeout or another warp's abort.
+// The global timer, slow to read, is looked at once in a thousand polls.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned err_bit, volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
+    if ((i & 1023u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      bool stop = *abort != 0;
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        report_error(err_bit);
+        *abort = 1;
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+  return true;
 }
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
@@ -322,8 +344,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       const int row0 = it.e * a.N + it.n0;
       for (int c = c0; c < c1; ++c, ++q) {
-        if (q >= WS) ok = mbar_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        if (q >= WS) ok = warp_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&wfull[s], uint32_t(S::CODE_BYTES));
@@ -356,8 +377,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
         zsrc[t] = a.zeros + row * zw;
       }
       for (int c = c0; c < c1; ++c, ++q) {
-        if (q >= WS) ok = mbar_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        if (q >= WS) ok = warp_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
         if (!ok) break;
         const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES) + uint32_t(lane * 16);
         const int at = c * sc_want, have = sc_stride - at;  // bytes past the row's end arrive as zeros
@@ -407,8 +427,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       for (int c = c0; c < c1 && ok; ++c) {
         const int nst = stages_of(c);
         for (int h = 0; h < nst; ++h, ++q) {
-          if (q >= XS) ok = mbar_wait(&mdone[s], par, ERR_TIMEOUT_PIPE, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
+          if (q >= XS) ok = warp_wait(&mdone[s], par, ERR_TIMEOUT_PIPE, abort_flag);
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&xfull[s], uint32_t(SK * boxes * S::XBOX) * 128u);
@@ -439,18 +458,18 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       const uint32_t idesc = idesc_bf16_f32(128, (it.rows + 15) & ~15);
       const int b = i % NACC, u = i / NACC;
-      if (u > 0) ok = mbar_wait(&dempty[b], (u - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      if (u > 0) ok = warp_wait(&dempty[b], (u - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
       if (!ok) break;
       const uint32_t acc = tmem + uint32_t(b * XT);
       uint32_t more = 0;
       for (int c = c0; c < c1 && ok; ++c) {
         const int nst = stages_of(c);
         for (int h = 0; h < nst; ++h, ++q) {
+          // both polled at once: in the steady state both are complete
           const bool xr = mbar_try_wait(&xfull[xs], xpar), ar = mbar_try_wait(&aready[as], apar);
-          ok = (xr || mbar_wait(&xfull[xs], xpar, ERR_TIMEOUT_TMA, abort_flag)) &&
-               (ar || mbar_wait(&aready[as], apar, ERR_TIMEOUT_PIPE, abort_flag));
-          ok = __all_sync(0xffffffffu, ok);
+          if (!__all_sync(0xffffffffu, xr && ar))
+            ok = warp_wait(&xfull[xs], xpar, ERR_TIMEOUT_TMA, abort_flag) &&
+                 warp_wait(&aready[as], apar, ERR_TIMEOUT_PIPE, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -483,67 +502,70 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     const int quarter = warp & 3;          // TMEM lanes of this warp
     const int trow = quarter * 32 + lane;  // weight row within the tile
     const uint32_t a_tmem = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(S::A_COL + (kb % SK) * 32);
-    int s = 0, q = 0;  // stage of the codes; stages of dequantized weights before this chunk
-    uint32_t wpar = 0;
+    const uint32_t my_codes = sbase + uint32_t(trow * 128);
+    const uint32_t my_meta = sbase + uint32_t(S::OFF_META + trow * 16);
+    // 16-byte pieces of this group's 32 bytes of a row, at their 128B-swizzled places
+    const uint32_t piece0 = uint32_t(((2 * kb) ^ (trow & 7)) << 4), piece1 = uint32_t(((2 * kb + 1) ^ (trow & 7)) << 4);
+    // byte within a row's chunk where this k-block's scales start
+    const int sc_at = FMT == GEMM_INT4 ? ((kb * 64) >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 4 * kb : 2 * kb;
+    int s = 0, as = 0, ms = 0;  // stage of the codes; stage of dequantized weights; slot whose MMAs free it
+    uint32_t wpar = 0, mpar = 0;
+    int q = kb / SK;            // this group's stage number; the first AS stages are free from the start
     bool ok = true;
+    as = q % AS;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
+      // row of the weights (mod 2^32: only its bytes' place within a word is asked for)
+      const uint32_t srow = uint32_t(it.e) * uint32_t(a.N) + uint32_t(min(it.n0 + trow, a.N - 1));
       for (int c = c0; c < c1; ++c) {
         const int nst = stages_of(c);
-        ok = mbar_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
         if (!ok) break;
-        const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
         uint32_t v[32];
         if (kb < nst * SK) {
-          const uint32_t codes = sbase + uint32_t(s * S::CODE_BYTES + trow * 128);
-          uint32_t w[8];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 16-byte pieces of the row, at their 128B-swizzled places
-            const uint4 p = ld_shared_v4(codes + uint32_t(((2 * kb + h) ^ (trow & 7)) << 4));
-            w[4 * h] = p.x; w[4 * h + 1] = p.y; w[4 * h + 2] = p.z; w[4 * h + 3] = p.w;
-          }
-          uint4 mv = ld_shared_v4(meta + uint32_t(trow * 16));
-          if (sc_align < 4) {
-            const uint32_t fifth = ld_shared_u32(meta + uint32_t(128 * 16 + trow * 4));
-            const uint32_t row = uint32_t(it.e) * uint32_t(a.N) + uint32_t(it.n0 + min(trow, a.N - 1 - it.n0));
-            const uint32_t sh = 8 * ((row * uint32_t(sc_stride) + uint32_t(c * sc_want)) & 3u);
-            mv.x = __funnelshift_r(mv.x, mv.y, sh);
-            mv.y = __funnelshift_r(mv.y, mv.z, sh);
-            mv.z = __funnelshift_r(mv.z, mv.w, sh);
-            mv.w = __funnelshift_r(mv.w, fifth, sh);
+          const uint4 w0 = ld_shared_v4(my_codes + uint32_t(s * S::CODE_BYTES) + piece0);
+          const uint4 w1 = ld_shared_v4(my_codes + uint32_t(s * S::CODE_BYTES) + piece1);
+          const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+          const uint32_t meta = my_meta + uint32_t(s * S::META_BYTES);
+          uint32_t sc;  // this k-block's scales
+          if (sc_align >= 4) {
+            sc = ld_shared_u32(meta + uint32_t(sc_at & ~3)) >> (8 * (sc_at & 3));
+          } else {  // the row starts inside a word: four bytes from any place
+            const uint32_t at = ((srow * uint32_t(sc_stride) + uint32_t(c * sc_want)) & 3u) + uint32_t(sc_at);
+            const uint32_t i = at >> 2;
+            const uint32_t fifth = meta + uint32_t(128 * 16 - 12 * trow);
+            sc = __funnelshift_r(ld_shared_u32(i < 4 ? meta + 4 * i : fifth), ld_shared_u32(i < 3 ? meta + 4 * i + 4 : fifth),
+                                 8 * (at & 3u));
           }
           if (FMT == GEMM_INT4) {
             uint32_t zword = 0x88888888u;
-            if (a.zeros) zword = ld_shared_u32(meta + uint32_t(128 * 20 + trow * 4));
-            zword >>= 4 * ((c * (kExpChunk >> a.log2g)) & 7);  // the chunk's first group in the low nibble
+            if (a.zeros) zword = ld_shared_u32(meta + uint32_t(128 * 20 - 12 * trow));
+            const int g0 = (c * kExpChunk + kb * 64) >> a.log2g;  // the k-block's first group
+            zword >>= 4 * (g0 & 7);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int g = (kb * 64 + h * 32) >> a.log2g;  // group within the chunk
-              const uint32_t word = g < 4 ? (g < 2 ? mv.x : mv.y) : (g < 6 ? mv.z : mv.w);
-              const uint32_t sc = g & 1 ? word >> 16 : word;
-              const float z = float((zword >> (4 * g)) & 15u);
-              const float cz = -16.f * (64.f + z) * __half2float(__ushort_as_half(uint16_t(sc)));
+              const bool second = h == 1 && a.log2g == 5;  // G = 32: two groups in the k-block
+              const uint32_t s16 = second ? sc >> 16 : sc;
+              const float z = float((second ? zword >> 4 : zword) & 15u);
+              const float cz = -16.f * (64.f + z) * __half2float(__ushort_as_half(uint16_t(s16)));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], sc, cz, v + 16 * h + 4 * j);
+              for (int j = 0; j < 4; ++j) dequant8_int4(w[4 * h + j], s16, cz, v + 16 * h + 4 * j);
             }
           } else if (FMT == GEMM_NVFP4) {
-            const uint32_t sb = kb < 2 ? (kb == 0 ? mv.x : mv.y) : (kb == 2 ? mv.z : mv.w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t s2;  // the scales of the two blocks, fp16 (exact)
               asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }"
-                  : "=r"(s2) : "r"((sb >> (16 * h)) & 0x7F7Fu));
+                  : "=r"(s2) : "r"((sc >> (16 * h)) & 0x7F7Fu));
               dequant8_e2m1<0>(w[4 * h], s2, v + 16 * h);
               dequant8_e2m1<0>(w[4 * h + 1], s2, v + 16 * h + 4);
               dequant8_e2m1<1>(w[4 * h + 2], s2, v + 16 * h + 8);
               dequant8_e2m1<1>(w[4 * h + 3], s2, v + 16 * h + 12);
             }
           } else {
-            const uint32_t sb = (kb < 2 ? mv.x : mv.y) >> (16 * (kb & 1));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t e8 = (sb >> (8 * h)) & 255u;
+              const uint32_t e8 = (sc >> (8 * h)) & 255u;
               // a scale that is a normal fp16 (2^-14 .. 2^15) for the whole warp, or fp32 products
               if (!a.inv_s && __all_sync(0xffffffffu, e8 - 113u < 30u)) {
                 const uint32_t s2 = (e8 - 112u) << 10;
@@ -559,20 +581,28 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
             }
           }
           // the columns are free once the MMAs of the stage AS back are done
-          const int n = q + kb / SK, p = n - AS, as = n % AS;
-          if (p >= 0) ok = mbar_wait(&mdone[p % XS], (p / XS) & 1, ERR_TIMEOUT_PIPE, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);  // tcgen05.st is warp-collective
-          if (!ok) break;
+          if (q >= AS) {
+            ok = warp_wait(&mdone[ms], mpar, ERR_TIMEOUT_PIPE, abort_flag);
+            if (!ok) break;
+          }
           tc_fence_after();
           tmem_st32(a_tmem + uint32_t(as * SK * 32), v);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&aready[as]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[s]);
-        q += nst;
+        if (lane == 0) {
+          if (kb < nst * SK) mbar_arrive(&aready[as]);
+          mbar_arrive(&wempty[s]);
+        }
+        // stages up to this group's place in the next chunk
+        for (int j = 0; j < nst; ++j) {
+          if (++as == AS) as = 0;
+          if (q++ >= AS && ++ms == XS) {
+            ms = 0;
+            mpar ^= 1u;
+          }
+        }
         if (++s == WS) {
           s = 0;
           wpar ^= 1u;
@@ -590,8 +620,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       const int b = i % NACC, u = i / NACC;
       const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + it.e) : FMT == GEMM_INT4 ? 0.0625f : 1.0f;
-      const bool go = mbar_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag);
-      if (!__all_sync(0xffffffffu, go)) break;
+      if (!warp_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag)) break;
       tc_fence_after();
       const int nw = it.n0 + quarter * 32;  // this warp's first weight row
       for (int x = 0; x < it.rows; x += 32) {
