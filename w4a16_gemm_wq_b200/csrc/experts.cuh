@@ -20,8 +20,8 @@
 //   warp 2       TMEM allocation and the MMA issuer (a whole warp in step, one
 //                elected lane issues: a lone lane's branch costs 46 clocks an
 //                instruction against 9 measured here)
-//   warp 3       the experts' row tiles, then the scales and zero points of the
-//                codes' rows by cp.async into the stages of the codes
+//   warp 3       the experts' row tiles, then the scales (SEG bytes a row at a time)
+//                and zero points of the codes' rows by cp.async, two segments deep
 //   warps 4-19   dequantizers: four groups of four warps, one 64-wide k-block of
 //                every chunk of 256 k each, into 32 columns of tensor memory
 //   warps 20-23  epilogue: tcgen05.ld, transpose in shared memory, store Y
@@ -61,19 +61,25 @@ constexpr int kExpGroups = 4;      // dequantizer groups: one k-block of a chunk
 // epilogue overlaps the next item); WS stages of codes.  X slots and stages of
 // dequantized weights hold SK k-blocks each: one pair of waits and one commit of the
 // MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.
-template <int XT_, int XBOX_, int NACC_, int WS_, int XS_, int SK_>
+//
+// Scales are fetched for many chunks at once, SEG bytes a row, because a warp's copy
+// of 4 bytes from each of 32 rows takes as long as one of 16 bytes (about 200 clocks,
+// more than the chunk's products).
+template <int XT_, int XBOX_, int NACC_, int WS_, int XS_, int SK_, int SEG_>
 struct ExpShape {
-  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_;
+  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_, SEG = SEG_;
   static constexpr int AS = SK == 1 ? 4 : 2;  // stages of dequantized weights, 32 SK columns each
   static constexpr int CODE_BYTES = 128 * 128;
-  static constexpr int META_BYTES = 128 * 24;  // per row 16 bytes of scales, a fifth word, a word of zero points
+  static constexpr int SC_PITCH = SEG + 16;     // a row's scales of a segment (a word more where rows start inside one)
+  static constexpr int Z_PITCH = SEG / 4 + 4;   // a row's zero points of a segment: SEG / 2 groups
+  static constexpr int META_BYTES = 128 * (SC_PITCH + Z_PITCH);
   static constexpr int SLOT_BYTES = SK * XT * 128;
   static constexpr int OFF_X = WS * CODE_BYTES;
   static constexpr int OFF_META = OFF_X + XS * SLOT_BYTES;
-  static constexpr int OFF_STAGE = OFF_META + WS * META_BYTES;
+  static constexpr int OFF_STAGE = OFF_META + 2 * META_BYTES;
   static constexpr int OFF_TAB = OFF_STAGE + 4 * 1024;
   static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxExperts + 4) * 4;
-  static constexpr int NBAR = 2 * WS + 2 * XS + AS + 2 * NACC;
+  static constexpr int NBAR = 2 * WS + 2 * XS + AS + 2 * NACC + 4;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr int A_COL = NACC * XT;
   static constexpr int USED_COLS = A_COL + AS * SK * 32;
@@ -81,11 +87,12 @@ struct ExpShape {
   static_assert(USED_COLS <= 512, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(XT % 16 == 0 && XT <= 256 && XT % XBOX == 0 && XBOX % 8 == 0, "row tiles");
+  static_assert(SEG == 32 || SEG == 64, "a chunk takes 4 to 16 bytes of scales");
   static_assert(4 % SK == 0 && XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
-using ExpWide = ExpShape<192, 32, 2, 3, 3, 2>;
-using ExpNarrow = ExpShape<64, 8, 2, 5, 3, 4>;
+using ExpWide = ExpShape<192, 32, 2, 3, 3, 2, 32>;
+using ExpNarrow = ExpShape<64, 8, 2, 5, 3, 4, 64>;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -228,23 +235,27 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   int* bound = reinterpret_cast<int*>(smem + S::OFF_TAB);  // [E + 1] rows of the experts
   int* tstart = bound + kMaxExperts + 4;                   // [E + 1] their first row tile
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-  uint64_t* wfull = bars;                 // codes and scales landed
+  uint64_t* wfull = bars;                 // codes landed
   uint64_t* wempty = wfull + WS;          // dequantizers are done with them
   uint64_t* xfull = wempty + WS;          // X boxes landed
   uint64_t* mdone = xfull + XS;           // MMAs of the k-block in this slot finished
   uint64_t* aready = mdone + XS;          // dequantized weights in tensor memory
   uint64_t* dfull = aready + AS;          // accumulator complete
   uint64_t* dempty = dfull + NACC;        // accumulator drained
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + NACC);
+  uint64_t* sfull = dempty + NACC;        // [2] a segment of scales landed
+  uint64_t* sempty = sfull + 2;           // [2] dequantizers are done with it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* bad_flag = reinterpret_cast<int*>(tmem_slot + 2);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == 0) {
-    for (int b = lane; b < S::NBAR; b += 32)
-      // arrivals: codes = the TMA's thread and the 32 lanes that copy the scales; one arrival a warp elsewhere
-      mbar_init(&bars[b], b < WS ? 33 : b < 2 * WS ? 4 * kExpGroups : b < 2 * (WS + XS) ? 1
-                          : b < 2 * (WS + XS) + AS ? 4 * SK : b < 2 * (WS + XS) + AS + NACC ? 1 : 4);
+    // arrivals: one of a thread that copies or commits, one of each dequantizer or epilogue warp
+    if (lane < WS) { mbar_init(&wfull[lane], 1); mbar_init(&wempty[lane], 4 * kExpGroups); }
+    if (lane < XS) { mbar_init(&xfull[lane], 1); mbar_init(&mdone[lane], 1); }
+    if (lane < AS) mbar_init(&aready[lane], 4 * SK);
+    if (lane < NACC) { mbar_init(&dfull[lane], 1); mbar_init(&dempty[lane], 4); }
+    if (lane < 2) { mbar_init(&sfull[lane], 32); mbar_init(&sempty[lane], 4 * kExpGroups); }
     fence_mbar_init();
     if (lane == 0) {
       *abort_flag = 0;
@@ -329,11 +340,12 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   };
   // stages of a chunk: whole ones, the k-blocks past K are zeros (of the codes, the scales and X)
   const auto stages_of = [&](int c) { return min(4 / SK, (a.K - c * kExpChunk + 64 * SK - 1) / (64 * SK)); };
-  // a row's scale bytes, those of a chunk, and the largest alignment that all chunks of all rows share
+  // a row's scale bytes, those of a chunk, and the alignment that all rows share
   const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
   const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
   const int sc_want = FMT == GEMM_INT4 ? (kExpChunk >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 16 : 8;
-  const int sc_align = (sc_stride | sc_want) & -(sc_stride | sc_want);
+  const int sc_align = (sc_stride & 15) == 0 ? 16 : (sc_stride & 3) == 0 ? 4 : 1;
+  const int cps = S::SEG / sc_want;  // chunks of a segment
 
   if (warp == 0) {
     // ---------------------------------------------------------- codes
@@ -362,57 +374,64 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------- scales and zero points
-    int q = 0, s = 0;
-    uint32_t par = 1;
+    int q = 0;
     bool ok = true;
     const int zw = ((a.K >> a.log2g) + 7) >> 3;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
-      const uint8_t* src[4];  // this lane's four rows: lane, lane + 32, ..
-      const uint32_t* zsrc[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int64_t row = int64_t(it.e) * a.N + min(it.n0 + lane + 32 * t, a.N - 1);
-        src[t] = sc_base + row * sc_stride;
-        zsrc[t] = a.zeros + row * zw;
-      }
-      for (int c = c0; c < c1; ++c, ++q) {
-        if (q >= WS) ok = warp_wait(&wempty[s], par, ERR_TIMEOUT_PIPE, abort_flag);
+      const int64_t row0 = int64_t(it.e) * a.N + it.n0;
+      const int valid = min(128, a.N - it.n0);  // rows past N get zeros
+      for (int c = c0; c < c1; c = (c / cps + 1) * cps, ++q) {
+        const int s = q & 1;
+        if (q >= 2) ok = warp_wait(&sempty[s], ((q >> 1) - 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
         if (!ok) break;
-        const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES) + uint32_t(lane * 16);
-        const int at = c * sc_want, have = sc_stride - at;  // bytes past the row's end arrive as zeros
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t dst = meta + uint32_t(t * 512);
-          const uint8_t* p = src[t] + at;
-          if (sc_align == 16) {
-            cp_async_zfill<16>(dst, p, uint32_t(min(16, have)));
-          } else if (sc_align == 8) {
-            cp_async_zfill<8>(dst, p, uint32_t(min(8, have)));
-            if (sc_want == 16) cp_async_zfill<8>(dst + 8, have > 8 ? p + 8 : p, uint32_t(max(0, min(8, have - 8))));
-          } else if (sc_align == 4) {
-#pragma unroll 1
-            for (int b = 0; b < sc_want; b += 4)
-              cp_async_zfill<4>(dst + b, b < have ? p + b : p, uint32_t(max(0, min(4, have - b))));
-          } else {
-            // rows that start inside a word: the words around the bytes, which the dequantizer shifts
-            const int off = int(reinterpret_cast<uintptr_t>(p) & 3), end = off + min(sc_want, have);
-#pragma unroll 1
-            for (int b = 0; b <= sc_want; b += 4) {
-              const int n = max(0, min(4, end - b));
-              cp_async_zfill<4>(b < 16 ? dst + b : meta + uint32_t(128 * 16 + t * 128) - uint32_t(lane * 12),
-                                p - off + (n ? b : 0), uint32_t(n));
+        const uint32_t meta = sbase + uint32_t(S::OFF_META + s * S::META_BYTES);
+        const int at = (c / cps) * S::SEG;                 // first byte of the segment within a row
+        const int have = min(S::SEG, sc_stride - at);      // bytes past the row's end arrive as zeros
+        if (sc_align == 16) {
+          constexpr int PR = S::SEG / 16;                  // 16-byte pieces a row
+          const int b = (lane % PR) * 16, n = max(0, min(16, have - b));
+          const uint8_t* p = sc_base + (row0 + lane / PR) * sc_stride + at + b;
+          uint32_t dst = meta + uint32_t((lane / PR) * S::SC_PITCH + b);
+#pragma unroll 4
+          for (int r = lane / PR; r < 128; r += 32 / PR, p += int64_t(32 / PR) * sc_stride, dst += 32 / PR * S::SC_PITCH) {
+            const bool in = r < valid && n > 0;
+            cp_async_zfill<16>(dst, in ? p : sc_base, in ? uint32_t(n) : 0u);
+          }
+        } else {
+          // words; rows that start inside one: the words around the bytes, which the dequantizer shifts
+          constexpr int PR = S::SEG / 4;
+          const int b = (lane % PR) * 4;
+          const uint8_t* p = sc_base + (row0 + lane / PR) * sc_stride + at;
+          uint32_t dst = meta + uint32_t((lane / PR) * S::SC_PITCH + b);
+#pragma unroll 4
+          for (int r = lane / PR; r < 128; r += 32 / PR, p += int64_t(32 / PR) * sc_stride, dst += 32 / PR * S::SC_PITCH) {
+            const int off = int(reinterpret_cast<uintptr_t>(p) & 3), n = max(0, min(4, off + have - b));
+            const bool in = r < valid && n > 0;
+            cp_async_zfill<4>(dst, in ? p - off + b : sc_base, in ? uint32_t(n) : 0u);
+          }
+          if (sc_align < 4) {
+            for (int r = lane; r < 128; r += 32) {
+              const uint8_t* e = sc_base + (row0 + r) * sc_stride + at;
+              const int off = int(reinterpret_cast<uintptr_t>(e) & 3), n = max(0, min(4, off + have - S::SEG));
+              const bool in = r < valid && n > 0;
+              cp_async_zfill<4>(meta + uint32_t(r * S::SC_PITCH + S::SEG), in ? e - off + S::SEG : sc_base,
+                                in ? uint32_t(n) : 0u);
             }
           }
-          if (FMT == GEMM_INT4 && a.zeros)
-            cp_async_zfill<4>(meta + uint32_t(128 * 20 + t * 128) - uint32_t(lane * 12),
-                              zsrc[t] + ((c * (kExpChunk >> a.log2g)) >> 3), 4);
         }
-        cp_async_arrive(&wfull[s]);
-        if (++s == WS) {
-          s = 0;
-          par ^= 1u;
+        if (FMT == GEMM_INT4 && a.zeros) {
+          constexpr int PR = S::SEG / 16;  // words of eight zero points a row
+          const int b = lane % PR, word = (c / cps) * PR + b;
+#pragma unroll 4
+          for (int r = lane / PR; r < 128; r += 32 / PR) {
+            const bool in = r < valid && word < zw;
+            cp_async_zfill<4>(meta + uint32_t(128 * S::SC_PITCH + r * S::Z_PITCH + b * 4),
+                              in ? a.zeros + (row0 + r) * zw + word : reinterpret_cast<const uint32_t*>(sc_base),
+                              in ? 4u : 0u);
+          }
         }
+        cp_async_arrive(&sfull[s]);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -503,12 +522,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     const int trow = quarter * 32 + lane;  // weight row within the tile
     const uint32_t a_tmem = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(S::A_COL + (kb % SK) * 32);
     const uint32_t my_codes = sbase + uint32_t(trow * 128);
-    const uint32_t my_meta = sbase + uint32_t(S::OFF_META + trow * 16);
+    const uint32_t my_scales = sbase + uint32_t(S::OFF_META + trow * S::SC_PITCH);
+    const uint32_t my_zeros = sbase + uint32_t(S::OFF_META + 128 * S::SC_PITCH + trow * S::Z_PITCH);
     // 16-byte pieces of this group's 32 bytes of a row, at their 128B-swizzled places
     const uint32_t piece0 = uint32_t(((2 * kb) ^ (trow & 7)) << 4), piece1 = uint32_t(((2 * kb + 1) ^ (trow & 7)) << 4);
     // byte within a row's chunk where this k-block's scales start
     const int sc_at = FMT == GEMM_INT4 ? ((kb * 64) >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 4 * kb : 2 * kb;
     int s = 0, as = 0, ms = 0;  // stage of the codes; stage of dequantized weights; slot whose MMAs free it
+    int sg = 0;                 // segments of scales so far
     uint32_t wpar = 0, mpar = 0;
     int q = kb / SK;            // this group's stage number; the first AS stages are free from the start
     bool ok = true;
@@ -517,31 +538,31 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       // row of the weights (mod 2^32: only its bytes' place within a word is asked for)
       const uint32_t srow = uint32_t(it.e) * uint32_t(a.N) + uint32_t(min(it.n0 + trow, a.N - 1));
-      for (int c = c0; c < c1; ++c) {
+      for (int c = c0, cs = c0 % cps; c < c1; ++c) {  // cs: chunk within its segment
         const int nst = stages_of(c);
-        ok = warp_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
+        if (c == c0 || cs == 0) ok = warp_wait(&sfull[sg & 1], (sg >> 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
+        ok = ok && warp_wait(&wfull[s], wpar, ERR_TIMEOUT_TMA, abort_flag);
         if (!ok) break;
         uint32_t v[32];
         if (kb < nst * SK) {
           const uint4 w0 = ld_shared_v4(my_codes + uint32_t(s * S::CODE_BYTES) + piece0);
           const uint4 w1 = ld_shared_v4(my_codes + uint32_t(s * S::CODE_BYTES) + piece1);
           const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-          const uint32_t meta = my_meta + uint32_t(s * S::META_BYTES);
-          uint32_t sc;  // this k-block's scales
+          const uint32_t meta = my_scales + uint32_t((sg & 1) * S::META_BYTES);
+          int at = cs * sc_want + sc_at;  // this k-block's scales within the segment
+          uint32_t sc;
           if (sc_align >= 4) {
-            sc = ld_shared_u32(meta + uint32_t(sc_at & ~3)) >> (8 * (sc_at & 3));
-          } else {  // the row starts inside a word: four bytes from any place
-            const uint32_t at = ((srow * uint32_t(sc_stride) + uint32_t(c * sc_want)) & 3u) + uint32_t(sc_at);
-            const uint32_t i = at >> 2;
-            const uint32_t fifth = meta + uint32_t(128 * 16 - 12 * trow);
-            sc = __funnelshift_r(ld_shared_u32(i < 4 ? meta + 4 * i : fifth), ld_shared_u32(i < 3 ? meta + 4 * i + 4 : fifth),
-                                 8 * (at & 3u));
+            sc = ld_shared_u32(meta + uint32_t(at & ~3)) >> (8 * (at & 3));
+          } else {  // the row starts inside a word (segments are whole words): four bytes from any place
+            at += int((srow * uint32_t(sc_stride)) & 3u);
+            sc = __funnelshift_r(ld_shared_u32(meta + uint32_t(at & ~3)), ld_shared_u32(meta + uint32_t((at & ~3) + 4)),
+                                 8 * (at & 3));
           }
           if (FMT == GEMM_INT4) {
             uint32_t zword = 0x88888888u;
-            if (a.zeros) zword = ld_shared_u32(meta + uint32_t(128 * 20 - 12 * trow));
-            const int g0 = (c * kExpChunk + kb * 64) >> a.log2g;  // the k-block's first group
-            zword >>= 4 * (g0 & 7);
+            const int g = (cs * kExpChunk + kb * 64) >> a.log2g;  // the k-block's first group within the segment
+            if (a.zeros) zword = ld_shared_u32(my_zeros + uint32_t((sg & 1) * S::META_BYTES + (g >> 3) * 4));
+            zword >>= 4 * (g & 7);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const bool second = h == 1 && a.log2g == 5;  // G = 32: two groups in the k-block
@@ -594,7 +615,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
         if (lane == 0) {
           if (kb < nst * SK) mbar_arrive(&aready[as]);
           mbar_arrive(&wempty[s]);
+          if (cs == cps - 1 || c == c1 - 1) mbar_arrive(&sempty[sg & 1]);
         }
+        if (++cs == cps) cs = 0;
+        if (cs == 0 || c == c1 - 1) ++sg;
         // stages up to this group's place in the next chunk
         for (int j = 0; j < nst; ++j) {
           if (++as == AS) as = 0;
