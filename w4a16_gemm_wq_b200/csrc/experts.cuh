@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include "gemm_tcgen05.cuh"
+#include "gemv_mma.cuh"
 #include "mxfp4.cuh"
 #include "wq_common.cuh"
 
@@ -43,6 +44,8 @@ constexpr int kExpChunk = 256;     // k per stage of codes (128 bytes a row)
 struct ExpertArgs {
   CUtensorMap tmW;         // codes u8 [E * N, K / 2], box {128, 128}, 128B swizzle
   CUtensorMap tmX;         // X bf16 [T, K], box {64, XBOX}, 128B swizzle
+  const uint16_t* X;       // bf16 [T, K]
+  const uint8_t* packed;   // K / 2 bytes per row, rows [E * N]
   const int* offsets;      // [E + 1], or null: one expert over all T rows
   const float* inv_s;      // fp32 [K] or null: multiplies column k of X (MXFP4 Linear)
   const uint16_t* scales;  // INT4 fp16 [E * N, K / G]
@@ -56,6 +59,54 @@ struct ExpertArgs {
 };
 
 constexpr int kExpGroups = 4;      // dequantizer groups: one k-block of a chunk each
+
+// Row bounds and first row tiles (of xt rows) of the experts, by one warp: bound[E + 1],
+// tstart[E + 1], *bad = offsets that decrease or leave [0, T] (then nothing is computed).
+__device__ __forceinline__ void expert_tables(const ExpertArgs& a, int xt, int* bound, int* tstart, int* bad_flag) {
+  const int lane = threadIdx.x & 31;
+  // each lane takes `per` experts in a row
+  const int per = (a.E + 31) >> 5, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
+  const auto bound_of = [&](int e) { return a.offsets ? __ldg(a.offsets + e) : (e ? a.T : 0); };
+  bool bad = false;
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int b0 = bound_of(e), b1 = bound_of(e + 1);
+    bad |= b0 < 0 || b1 < b0 || b1 > a.T;
+    sum += bad ? 0 : (b1 - b0 + xt - 1) / xt;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  int t = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, t, off);
+    if (lane >= off) t += v;
+  }
+  t -= sum;
+  for (int e = e0; e < e1; ++e) {
+    const int b0 = bound_of(e), b1 = bound_of(e + 1);
+    bound[e] = b0;
+    tstart[e] = t;
+    t += bad ? 0 : (b1 - b0 + xt - 1) / xt;
+    if (e == a.E - 1) {
+      bound[a.E] = b1;
+      tstart[a.E] = t;
+    }
+  }
+  if (lane == 0) {
+    *bad_flag = bad;
+    if (bad && blockIdx.x == 0) report_error(ERR_OFFSETS);
+  }
+}
+
+// The last e with tstart[e] <= tile: the expert of a row tile.
+__device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tstart[mid] <= tile) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 
 // Up to XT rows of X per item, in boxes of XBOX; NACC accumulators (2: the
 // epilogue overlaps the next item); WS stages of codes.  X slots and stages of
@@ -269,38 +320,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 3) {
-    // row bounds and first row tiles of the experts: each lane takes `per` of them in a row
-    const int per = (a.E + 31) >> 5, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
-    const auto bound_of = [&](int e) { return a.offsets ? __ldg(a.offsets + e) : (e ? a.T : 0); };
-    bool bad = false;
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) {
-      const int b0 = bound_of(e), b1 = bound_of(e + 1);
-      bad |= b0 < 0 || b1 < b0 || b1 > a.T;
-      sum += (b1 - b0 + XT - 1) / XT;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    int t = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, t, off);
-      if (lane >= off) t += v;
-    }
-    t -= sum;
-    for (int e = e0; e < e1; ++e) {
-      const int b0 = bound_of(e), b1 = bound_of(e + 1);
-      bound[e] = b0;
-      tstart[e] = t;
-      t += (b1 - b0 + XT - 1) / XT;
-      if (e == a.E - 1) {
-        bound[a.E] = b1;
-        tstart[a.E] = t;
-      }
-    }
-    if (lane == 0) {
-      *bad_flag = bad;
-      if (bad && blockIdx.x == 0) report_error(ERR_OFFSETS);
-    }
+    expert_tables(a, XT, bound, tstart, bad_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -326,11 +346,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     Item it;
     const int tt = id / nblocks;
     it.n0 = (id - tt * nblocks) * 128;
-    int lo = 0, hi = a.E;  // the last e with tstart[e] <= tt
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tstart[mid] <= tt) lo = mid; else hi = mid;
-    }
+    const int lo = expert_of_tile(tstart, a.E, tt);
     it.e = lo;
     const int r = bound[lo + 1] - bound[lo], t = tstart[lo + 1] - tstart[lo];
     const int w = ((r + t - 1) / t + 15) & ~15;  // the expert's rows, evenly over its tiles
@@ -720,6 +736,265 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, S::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per expert: mma.sync with the weights (16 rows of W_e) as the A operand,
+// dequantized in registers, and up to 8 NT rows of X as B.  Bound by HBM (0.53 to
+// 0.63 bytes a weight) and by the dequantization's instructions, both within 20%.
+//
+// A unit is 16 weight rows of one row tile; its steps are 128 k each.  A CTA takes a
+// contiguous share of the units, its warps contiguous shares of the CTA's steps, so that
+// every SM streams the same number of bytes whatever K is, and only units that
+// straddle warps are summed through shared memory, in warp order.  A step's codes come
+// by cp.async, kVecDepth steps ahead, into slots that the copying lane reads itself
+// (no barrier, and a loop body of one step: the kernel is short, and a body unrolled
+// over the steps in flight spent most of it on instruction fetches); scales and a
+// word's rows of X one step ahead into registers (L2 holds the scales' sector from the
+// first step that touched it, L1 the rows that all warps of a CTA read).
+// Lane (g, c) (g = lane / 4, c = lane % 4) holds codes of rows g and g + 8: the k order
+// inside an MMA is free, so its four k of each are four consecutive k of the lane's.
+//   INT4   lane c takes G / 4 k of every group, so that an MMA stays inside a group: A is
+//          q - z (exact in bf16), and the fp16 scale multiplies the group's fp32 sums;
+//   E2M1   lane c takes 32 k in a row; A is the code times its block scale, exact in bf16.
+constexpr int kVecWarps = 16;
+constexpr int kVecDepth = 6;
+constexpr int kVecSmem = kVecWarps * kVecDepth * 1024;
+
+__device__ __forceinline__ uint32_t ldg_u16(const void* p) { return __ldg(static_cast<const uint16_t*>(p)); }
+__device__ __forceinline__ uint32_t ldg_u8(const void* p) { return __ldg(static_cast<const uint8_t*>(p)); }
+
+template <int FMT, int G, int NT>
+__global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __grid_constant__ ExpertArgs a) {
+  static_assert(FMT != GEMM_INT4 || G == 32 || G == 64 || G == 128, "group size");
+  constexpr int NG = FMT == GEMM_INT4 ? 128 / G : 1;    // groups of a step
+  constexpr int WPG = 4 / NG;                           // words (8 k) of a lane per group
+  __shared__ int bound[kMaxExperts + 4], tstart[kMaxExperts + 4];
+  __shared__ int bad_flag;
+  __shared__ float part[2 * kVecWarps][16][8 * NT];     // sums of units that straddle warps
+  extern __shared__ __align__(16) uint8_t vec_smem[];   // codes: [warp][kVecDepth][2][32 lanes][16 bytes]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int K = a.K, N = a.N;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) expert_tables(a, 8 * NT, bound, tstart, &bad_flag);
+  __syncthreads();
+  if (bad_flag) return;
+  const int nrb = (N + 15) >> 4, S = (K + 127) >> 7;  // row blocks of an expert, steps of a unit
+  const int units = tstart[a.E] * nrb;
+  const int u0 = int(int64_t(units) * blockIdx.x / gridDim.x), u1 = int(int64_t(units) * (blockIdx.x + 1) / gridDim.x);
+  const int64_t tot = int64_t(u1 - u0) * S;
+  const auto first_of = [&](int w) { return tot * w / kVecWarps; };  // first step of warp w
+
+  struct Unit {
+    int e, row, rows, n0;
+  };
+  const auto unit_of = [&](int u) {
+    Unit t;
+    const int tile = u / nrb;
+    t.n0 = (u - tile * nrb) * 16;
+    t.e = expert_of_tile(tstart, a.E, tile);
+    const int r = bound[t.e + 1] - bound[t.e], nt = tstart[t.e + 1] - tstart[t.e];
+    const int w = (r + nt - 1) / nt;  // the expert's rows, evenly over its tiles
+    t.row = bound[t.e] + (tile - tstart[t.e]) * w;
+    t.rows = min(w, bound[t.e + 1] - t.row);
+    return t;
+  };
+  // k of word j (8 codes) of this lane within a step
+  const auto k_of = [&](int j) { return FMT == GEMM_INT4 ? (j / WPG) * G + c * (G / 4) + (j % WPG) * 8 : 32 * c + 8 * j; };
+  const int zw = (((FMT == GEMM_INT4 ? K / G : 8) + 7) >> 3) * 4;  // zero-point bytes of a row
+  const int sw = FMT == GEMM_INT4 ? K / G * 2 : FMT == GEMM_NVFP4 ? K >> 4 : K >> 5;  // scale bytes of a row
+  const uint8_t* sbase = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
+
+  const uint32_t ring = smem_u32(vec_smem) + uint32_t(warp * kVecDepth * 1024 + lane * 16);
+  int64_t at = first_of(warp);
+  const int64_t end = first_of(warp + 1);
+  while (at < end) {
+    // ---- the warp's steps [ja, jb) of a unit
+    const int u = int(at / S), ja = int(at - int64_t(u) * S), jb = int(min(int64_t(S), ja + (end - at)));
+    at += jb - ja;
+    const Unit t = unit_of(u0 + u);
+    const int64_t rlo = int64_t(t.e) * N + min(t.n0 + g, N - 1), rhi = int64_t(t.e) * N + min(t.n0 + g + 8, N - 1);
+    const uint8_t* plo = a.packed + rlo * (K >> 1);
+    const uint8_t* phi = a.packed + rhi * (K >> 1);
+    const uint8_t* slo = sbase + rlo * sw;
+    const uint8_t* shi = sbase + rhi * sw;
+    const uint8_t* zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
+    const uint8_t* zhi = reinterpret_cast<const uint8_t*>(a.zeros) + rhi * zw;
+    const uint16_t* xp[NT];  // this lane's rows of X (null: no such row)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xp[n] = 8 * n + g < t.rows ? a.X + int64_t(t.row + 8 * n + g) * K : nullptr;
+
+    // a lane's 16 code bytes of each row, in word order; zeros past K
+    const auto request = [&](int j) {
+      const int k0 = j * 128;
+      const uint32_t dst = ring + uint32_t(j % kVecDepth) * 1024u;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const int b = (k0 >> 1) + (FMT == GEMM_INT4 ? i * (G / 2) + c * (G / 8) : 16 * c);
+        const bool in = FMT == GEMM_INT4 ? k0 + i * G < K : k0 + 32 * c < K;
+        cp_async_zfill<16 / NG>(dst + i * (16 / NG), plo + (in ? b : 0), in ? 16 / NG : 0);
+        cp_async_zfill<16 / NG>(dst + 512 + i * (16 / NG), phi + (in ? b : 0), in ? 16 / NG : 0);
+      }
+    };
+    // scales, row g's in the low half (fp16 per group, two E4M3 bytes, or an E8M0 byte), and
+    // the bytes that hold the step's zero points (one for G >= 64, else two)
+    uint32_t sc[NG], zp = 0x88888888u;
+    const auto load_scales = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const int b = FMT == GEMM_INT4 ? (j * NG + i) * 2 : FMT == GEMM_NVFP4 ? 8 * j + 2 * c : 4 * j + c;
+        sc[i] = b >= sw ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo + b) | (ldg_u8(shi + b) << 16)
+                                                 : ldg_u16(slo + b) | (ldg_u16(shi + b) << 16);
+      }
+      if (FMT == GEMM_INT4 && a.zeros) {
+        const int b = (j * NG) >> 1;
+        zp = G == 32 ? ldg_u16(zlo + b) | (ldg_u16(zhi + b) << 16) : ldg_u8(zlo + b) | (ldg_u8(zhi + b) << 16);
+      }
+    };
+    const auto xload = [&](int n, int w, int j) {
+      const int k = j * 128 + k_of(w);
+      return xp[n] && k < K ? ldg_v4(xp[n] + k) : make_uint4(0, 0, 0, 0);
+    };
+
+    uint4 x[NT][4];
+    float acc[NT][4];
+#pragma unroll 1
+    for (int i = 0; i < kVecDepth - 1; ++i) {
+      if (ja + i < jb) request(ja + i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    load_scales(ja);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x[n][w] = xload(n, w, ja);
+      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    }
+#pragma unroll 1
+    for (int j = ja; j < jb; ++j) {
+      if (j + kVecDepth - 1 < jb) request(j + kVecDepth - 1);
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kVecDepth - 1) : "memory");
+      const uint32_t slot = ring + uint32_t(j % kVecDepth) * 1024u;
+      const uint4 cl = ld_shared_v4(slot), ch = ld_shared_v4(slot + 512);
+      const uint32_t wl[4] = {cl.x, cl.y, cl.z, cl.w}, wh[4] = {ch.x, ch.y, ch.z, ch.w};
+      uint32_t s[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) s[i] = sc[i];
+      const uint32_t z = zp;
+      if (j + 1 < jb) load_scales(j + 1);
+      uint32_t s2lo = 0, s2hi = 0;
+      bool f16 = true;  // MXFP4: the warp's block scales are normal fp16 values
+      if (FMT == GEMM_NVFP4) {
+        s2lo = tc_e4m3x2(s[0] & 0x7F7Fu);
+        s2hi = tc_e4m3x2((s[0] >> 16) & 0x7F7Fu);
+      } else if (FMT == GEMM_MXFP4) {
+        const uint32_t el = s[0] & 255u, eh = s[0] >> 16;
+        f16 = __all_sync(0xffffffffu, el - 113u < 30u && eh - 113u < 30u);
+        s2lo = f16 ? (el - 112u) << 10 : __float_as_uint(e8m0_f32(el));
+        s2hi = f16 ? (eh - 112u) << 10 : __float_as_uint(e8m0_f32(eh));
+      }
+      float d[NT][4];  // INT4: the group's sums
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t al[4], ah[4];
+        if (FMT == GEMM_INT4) {
+          const int nib = 4 * ((G == 128 ? (j & 1) : 0) + w / WPG);  // this group's zero point
+          const uint32_t zl = 0x43004300u + ((z >> nib) & 15u) * 0x00010001u;
+          const uint32_t zh = 0x43004300u + ((z >> (16 + nib)) & 15u) * 0x00010001u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // {code q, code q + 4}
+            al[q] = bf16x2_sub(lop3_andor(wl[w] >> (4 * q), 0x000F000Fu, 0x43004300u), zl);
+            ah[q] = bf16x2_sub(lop3_andor(wh[w] >> (4 * q), 0x000F000Fu, 0x43004300u), zh);
+          }
+        } else if (FMT == GEMM_NVFP4) {
+          if (w < 2) {
+            dequant8_e2m1<0>(wl[w], s2lo, al);
+            dequant8_e2m1<0>(wh[w], s2hi, ah);
+          } else {
+            dequant8_e2m1<1>(wl[w], s2lo, al);
+            dequant8_e2m1<1>(wh[w], s2hi, ah);
+          }
+        } else if (f16) {
+          dequant8_e2m1<0>(wl[w], s2lo, al);
+          dequant8_e2m1<0>(wh[w], s2hi, ah);
+        } else {
+          dequant8_e2m1_f32(wl[w], __uint_as_float(s2lo), nullptr, al);
+          dequant8_e2m1_f32(wh[w], __uint_as_float(s2hi), nullptr, ah);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint4 b = x[n][w];
+          if (j + 1 < jb) x[n][w] = xload(n, w, j + 1);
+          const int k = j * 128 + k_of(w);
+          if (FMT == GEMM_MXFP4 && a.inv_s && k < K) {  // X * act_inv_s, rounded to bf16 once
+            const float4 i0 = __ldg(reinterpret_cast<const float4*>(a.inv_s + k));
+            const float4 i1 = __ldg(reinterpret_cast<const float4*>(a.inv_s + k) + 1);
+            b.x = pack_bf16x2(__uint_as_float(b.x << 16) * i0.x, __uint_as_float(b.x & 0xFFFF0000u) * i0.y);
+            b.y = pack_bf16x2(__uint_as_float(b.y << 16) * i0.z, __uint_as_float(b.y & 0xFFFF0000u) * i0.w);
+            b.z = pack_bf16x2(__uint_as_float(b.z << 16) * i1.x, __uint_as_float(b.z & 0xFFFF0000u) * i1.y);
+            b.w = pack_bf16x2(__uint_as_float(b.w << 16) * i1.z, __uint_as_float(b.w & 0xFFFF0000u) * i1.w);
+          }
+          if (FMT == GEMM_INT4) {
+            if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+            // {x0, x4} {x1, x5} | {x2, x6} {x3, x7}
+            mma_bf16_16816(d[n], al[0], ah[0], al[1], ah[1], prmt_b32(b.x, b.z, 0x5410), prmt_b32(b.x, b.z, 0x7632));
+            mma_bf16_16816(d[n], al[2], ah[2], al[3], ah[3], prmt_b32(b.y, b.w, 0x5410), prmt_b32(b.y, b.w, 0x7632));
+            if (w % WPG == WPG - 1) {
+              const float sl = __half2float(__ushort_as_half(uint16_t(s[w / WPG])));
+              const float sh = __half2float(__ushort_as_half(uint16_t(s[w / WPG] >> 16)));
+              acc[n][0] = fmaf(sl, d[n][0], acc[n][0]);
+              acc[n][1] = fmaf(sl, d[n][1], acc[n][1]);
+              acc[n][2] = fmaf(sh, d[n][2], acc[n][2]);
+              acc[n][3] = fmaf(sh, d[n][3], acc[n][3]);
+            }
+          } else {
+            mma_bf16_16816(acc[n], al[0], ah[0], al[1], ah[1], b.x, b.y);
+            mma_bf16_16816(acc[n], al[2], ah[2], al[3], ah[3], b.z, b.w);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // ---- rows g and g + 8, columns 8 n + 2 c (+ 1): the unit's result, or the warp's share of it
+    if (ja == 0 && jb == S) {
+      const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + t.e) : 1.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = 8 * n + 2 * c + (q & 1), r = t.n0 + g + (q >> 1) * 8;
+          const float y = acc[n][q] * gmul;
+          if (m < t.rows && r < N) a.Y[int64_t(t.row + m) * N + r] = uint16_t(pack_bf16x2(y, y));
+        }
+    } else {
+      // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: a later one ends it
+      float (*p)[8 * NT] = part[2 * warp + (ja == 0)];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[g + (q >> 1) * 8][8 * n + 2 * c + (q & 1)] = acc[n][q];
+    }
+  }
+  __syncthreads();
+  // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
+  const int64_t s0 = first_of(warp);
+  const int u = int(s0 / S);
+  const int64_t ub = int64_t(u) * S;  // the unit's first step
+  if (s0 < end && s0 > ub && end >= ub + S) {
+    int v = warp - 1;
+    while (first_of(v) > ub) --v;
+    const Unit t = unit_of(u0 + u);
+    const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + t.e) : 1.f;
+    for (int i = lane; i < 16 * 8 * NT; i += 32) {
+      const int r = i & 15, m = i >> 4;
+      float y = 0.f;
+      for (int w = v; w <= warp; ++w)
+        if (first_of(w) < first_of(w + 1)) y += part[2 * w + (first_of(w) <= ub)][r][m];
+      y *= gmul;
+      if (m < t.rows && t.n0 + r < N) a.Y[int64_t(t.row + m) * N + t.n0 + r] = uint16_t(pack_bf16x2(y, y));
+    }
   }
 }
 

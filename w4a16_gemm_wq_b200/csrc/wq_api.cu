@@ -610,6 +610,33 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
   return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
 }
 
+// The mma.sync form for few rows per expert: one CTA per SM over units of 16 weight rows.
+template <int FMT, int G, int NT>
+int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
+  const int64_t holders = std::min(a.E, a.T);
+  const int64_t units = (holders + a.T / (8 * NT)) * ((int64_t(a.N) + 15) / 16);
+  static std::atomic<uint64_t> attr_done{0};
+  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT>, wq::kVecSmem, &attr_done, "expert gemv smem attribute"))
+    return e;
+  return launch_pdl(wq::expert_gemv_kernel<FMT, G, NT>, dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas))),
+                    dim3(wq::kVecWarps * 32), wq::kVecSmem, st, "expert gemv launch", a);
+}
+
+template <int FMT, int G>
+int launch_expert_gemv_g(const wq::ExpertArgs& a, cudaStream_t st) {
+  return a.T <= 8 * std::min(a.E, a.T) ? launch_expert_gemv_nt<FMT, G, 1>(a, st) : launch_expert_gemv_nt<FMT, G, 2>(a, st);
+}
+
+template <int FMT>
+int launch_expert_gemv(const wq::ExpertArgs& a, cudaStream_t st) {
+  if constexpr (FMT == wq::GEMM_INT4)
+    return a.log2g == 5   ? launch_expert_gemv_g<FMT, 32>(a, st)
+           : a.log2g == 6 ? launch_expert_gemv_g<FMT, 64>(a, st)
+                          : launch_expert_gemv_g<FMT, 128>(a, st);
+  else
+    return launch_expert_gemv_g<FMT, 0>(a, st);
+}
+
 template <int FMT>
 int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* packed, cudaStream_t st) {
   // the host does not know how the rows fall on the experts: at most min(E, T) hold any, and
@@ -617,6 +644,11 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   const int64_t holders = std::min(a.E, a.T);
   const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
   if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(192), st);
+  if (a.T / holders <= 16) {
+    wq::ExpertArgs v = a;
+    v.X = X; v.packed = static_cast<const uint8_t*>(packed);
+    return launch_expert_gemv<FMT>(v, st);
+  }
   const int64_t n = items(64);
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
   const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
