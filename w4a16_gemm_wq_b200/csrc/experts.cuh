@@ -759,13 +759,14 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 //          q - z (exact in bf16), and the fp16 scale multiplies the group's fp32 sums;
 //   E2M1   lane c takes 32 k in a row; A is the code times its block scale, exact in bf16.
 constexpr int kVecWarps = 16;
-constexpr int kVecDepth = 6;
+constexpr int kVecDepth = 4;
 constexpr int kVecSmem = kVecWarps * kVecDepth * 1024;
 
+// FULL: K % 128 == 0, no step reaches past K (and scale bytes of a step are aligned words).
 __device__ __forceinline__ uint32_t ldg_u16(const void* p) { return __ldg(static_cast<const uint16_t*>(p)); }
 __device__ __forceinline__ uint32_t ldg_u8(const void* p) { return __ldg(static_cast<const uint8_t*>(p)); }
 
-template <int FMT, int G, int NT>
+template <int FMT, int G, int NT, bool FULL>
 __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __grid_constant__ ExpertArgs a) {
   static_assert(FMT != GEMM_INT4 || G == 32 || G == 64 || G == 128, "group size");
   constexpr int NG = FMT == GEMM_INT4 ? 128 / G : 1;    // groups of a step
@@ -782,10 +783,11 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   __syncthreads();
   if (bad_flag) return;
   const int nrb = (N + 15) >> 4, S = (K + 127) >> 7;  // row blocks of an expert, steps of a unit
-  const int units = tstart[a.E] * nrb;
-  const int u0 = int(int64_t(units) * blockIdx.x / gridDim.x), u1 = int(int64_t(units) * (blockIdx.x + 1) / gridDim.x);
-  const int64_t tot = int64_t(u1 - u0) * S;
-  const auto first_of = [&](int w) { return tot * w / kVecWarps; };  // first step of warp w
+  // the CTA's units and the warps' first steps of them
+  const int units = tstart[a.E] * nrb, per = units / gridDim.x, more = units - per * gridDim.x;
+  const int u0 = blockIdx.x * per + min(int(blockIdx.x), more), nu = per + (int(blockIdx.x) < more);
+  const int tot = nu * S;
+  const auto first_of = [&](int w) { return int(int64_t(tot) * w / kVecWarps); };
 
   struct Unit {
     int e, row, rows, n0;
@@ -808,54 +810,70 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   const uint8_t* sbase = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
 
   const uint32_t ring = smem_u32(vec_smem) + uint32_t(warp * kVecDepth * 1024 + lane * 16);
-  int64_t at = first_of(warp);
-  const int64_t end = first_of(warp + 1);
+  int at = first_of(warp);
+  const int end = first_of(warp + 1);
   while (at < end) {
     // ---- the warp's steps [ja, jb) of a unit
-    const int u = int(at / S), ja = int(at - int64_t(u) * S), jb = int(min(int64_t(S), ja + (end - at)));
+    const int u = at / S, ja = at - u * S, jb = min(S, ja + end - at);
     at += jb - ja;
     const Unit t = unit_of(u0 + u);
     const int64_t rlo = int64_t(t.e) * N + min(t.n0 + g, N - 1), rhi = int64_t(t.e) * N + min(t.n0 + g + 8, N - 1);
-    const uint8_t* plo = a.packed + rlo * (K >> 1);
-    const uint8_t* phi = a.packed + rhi * (K >> 1);
-    const uint8_t* slo = sbase + rlo * sw;
-    const uint8_t* shi = sbase + rhi * sw;
+    // cursors: codes kVecDepth - 1 steps ahead, scales and X one step ahead
+    const uint8_t* plo = a.packed + rlo * (K >> 1) + ja * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
+    const uint8_t* phi = plo + (rhi - rlo) * (K >> 1);
+    constexpr int SB = FMT == GEMM_INT4 ? 2 * NG : FMT == GEMM_NVFP4 ? 8 : 4;  // scale bytes of a step
+    const uint8_t* slo = sbase + rlo * sw + ja * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
+    const uint8_t* shi = slo + (rhi - rlo) * sw;
     const uint8_t* zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
-    const uint8_t* zhi = reinterpret_cast<const uint8_t*>(a.zeros) + rhi * zw;
-    const uint16_t* xp[NT];  // this lane's rows of X (null: no such row)
+    const uint8_t* zhi = zlo + (rhi - rlo) * zw;
+    const uint16_t* xp[NT];  // this lane's rows of X; a lane without one reads the tile's last (its sums are not stored)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xp[n] = 8 * n + g < t.rows ? a.X + int64_t(t.row + 8 * n + g) * K : nullptr;
+    for (int n = 0; n < NT; ++n)
+      xp[n] = a.X + int64_t(t.row + min(8 * n + g, t.rows - 1)) * K + ja * 128 + (FMT == GEMM_INT4 ? c * (G / 4) : 32 * c);
 
     // a lane's 16 code bytes of each row, in word order; zeros past K
+    uint32_t put = ring + uint32_t(ja % kVecDepth) * 1024u;
     const auto request = [&](int j) {
-      const int k0 = j * 128;
-      const uint32_t dst = ring + uint32_t(j % kVecDepth) * 1024u;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const int b = (k0 >> 1) + (FMT == GEMM_INT4 ? i * (G / 2) + c * (G / 8) : 16 * c);
-        const bool in = FMT == GEMM_INT4 ? k0 + i * G < K : k0 + 32 * c < K;
-        cp_async_zfill<16 / NG>(dst + i * (16 / NG), plo + (in ? b : 0), in ? 16 / NG : 0);
-        cp_async_zfill<16 / NG>(dst + 512 + i * (16 / NG), phi + (in ? b : 0), in ? 16 / NG : 0);
+        const bool in = FULL || (FMT == GEMM_INT4 ? j * 128 + i * G < K : j * 128 + 32 * c < K);
+        cp_async_zfill<16 / NG>(put + i * (16 / NG), in ? plo + i * (G / 2) : a.packed, in ? 16 / NG : 0);
+        cp_async_zfill<16 / NG>(put + 512 + i * (16 / NG), in ? phi + i * (G / 2) : a.packed, in ? 16 / NG : 0);
       }
+      plo += 64;
+      phi += 64;
+      put = put + 1024u == ring + kVecDepth * 1024u ? ring : put + 1024u;
     };
     // scales, row g's in the low half (fp16 per group, two E4M3 bytes, or an E8M0 byte), and
     // the bytes that hold the step's zero points (one for G >= 64, else two)
     uint32_t sc[NG], zp = 0x88888888u;
     const auto load_scales = [&](int j) {
+      if (FMT == GEMM_INT4 && FULL && NG > 1) {  // a row's scales of the step as words
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const int b = FMT == GEMM_INT4 ? (j * NG + i) * 2 : FMT == GEMM_NVFP4 ? 8 * j + 2 * c : 4 * j + c;
-        sc[i] = b >= sw ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo + b) | (ldg_u8(shi + b) << 16)
-                                                 : ldg_u16(slo + b) | (ldg_u16(shi + b) << 16);
+        for (int i = 0; i < NG; i += 2) {
+          const uint32_t l = __ldg(reinterpret_cast<const uint32_t*>(slo + 2 * i));
+          const uint32_t h = __ldg(reinterpret_cast<const uint32_t*>(shi + 2 * i));
+          sc[i] = prmt_b32(l, h, 0x5410);
+          sc[(i + 1) % NG] = prmt_b32(l, h, 0x7632);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const bool in = FULL || (FMT == GEMM_INT4 ? (j * NG + i) * 2 < sw : j * 128 + 32 * c < K);
+          sc[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) | (ldg_u8(shi) << 16)
+                                               : ldg_u16(slo + 2 * i) | (ldg_u16(shi + 2 * i) << 16);
+        }
       }
+      slo += SB;
+      shi += SB;
       if (FMT == GEMM_INT4 && a.zeros) {
         const int b = (j * NG) >> 1;
         zp = G == 32 ? ldg_u16(zlo + b) | (ldg_u16(zhi + b) << 16) : ldg_u8(zlo + b) | (ldg_u8(zhi + b) << 16);
       }
     };
     const auto xload = [&](int n, int w, int j) {
-      const int k = j * 128 + k_of(w);
-      return xp[n] && k < K ? ldg_v4(xp[n] + k) : make_uint4(0, 0, 0, 0);
+      const int k = FMT == GEMM_INT4 ? (w / WPG) * G + (w % WPG) * 8 : 8 * w;  // past the lane's first of the step
+      return FULL || j * 128 + k_of(w) < K ? ldg_v4(xp[n] + k) : make_uint4(0, 0, 0, 0);
     };
 
     uint4 x[NT][4];
@@ -866,18 +884,20 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
     load_scales(ja);
+    uint32_t take = ring + uint32_t(ja % kVecDepth) * 1024u;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) x[n][w] = xload(n, w, ja);
+      xp[n] += 128;
       acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
     }
 #pragma unroll 1
     for (int j = ja; j < jb; ++j) {
       if (j + kVecDepth - 1 < jb) request(j + kVecDepth - 1);
       asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kVecDepth - 1) : "memory");
-      const uint32_t slot = ring + uint32_t(j % kVecDepth) * 1024u;
-      const uint4 cl = ld_shared_v4(slot), ch = ld_shared_v4(slot + 512);
+      const uint4 cl = ld_shared_v4(take), ch = ld_shared_v4(take + 512);
+      take = take + 1024u == ring + kVecDepth * 1024u ? ring : take + 1024u;
       const uint32_t wl[4] = {cl.x, cl.y, cl.z, cl.w}, wh[4] = {ch.x, ch.y, ch.z, ch.w};
       uint32_t s[NG];
 #pragma unroll
@@ -955,6 +975,8 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xp[n] += 128;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     // ---- rows g and g + 8, columns 8 n + 2 c (+ 1): the unit's result, or the warp's share of it
@@ -979,9 +1001,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   }
   __syncthreads();
   // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
-  const int64_t s0 = first_of(warp);
-  const int u = int(s0 / S);
-  const int64_t ub = int64_t(u) * S;  // the unit's first step
+  const int s0 = first_of(warp), u = s0 / S, ub = u * S;  // the unit of the warp's first step, and that unit's first
   if (s0 < end && s0 > ub && end >= ub + S) {
     int v = warp - 1;
     while (first_of(v) > ub) --v;

@@ -611,20 +611,28 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
 }
 
 // The mma.sync form for few rows per expert: one CTA per SM over units of 16 weight rows.
-template <int FMT, int G, int NT>
-int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
+template <int FMT, int G, int NT, bool FULL>
+int launch_expert_gemv_full(const wq::ExpertArgs& a, cudaStream_t st) {
   const int64_t holders = std::min(a.E, a.T);
   const int64_t units = (holders + a.T / (8 * NT)) * ((int64_t(a.N) + 15) / 16);
   static std::atomic<uint64_t> attr_done{0};
-  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT>, wq::kVecSmem, &attr_done, "expert gemv smem attribute"))
+  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT, FULL>, wq::kVecSmem, &attr_done,
+                               "expert gemv smem attribute"))
     return e;
-  return launch_pdl(wq::expert_gemv_kernel<FMT, G, NT>, dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas))),
+  return launch_pdl(wq::expert_gemv_kernel<FMT, G, NT, FULL>, dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas))),
                     dim3(wq::kVecWarps * 32), wq::kVecSmem, st, "expert gemv launch", a);
+}
+
+template <int FMT, int G, int NT>
+int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
+  return a.K % 128 == 0 ? launch_expert_gemv_full<FMT, G, NT, true>(a, st)
+                        : launch_expert_gemv_full<FMT, G, NT, false>(a, st);
 }
 
 template <int FMT, int G>
 int launch_expert_gemv_g(const wq::ExpertArgs& a, cudaStream_t st) {
-  return a.T <= 8 * std::min(a.E, a.T) ? launch_expert_gemv_nt<FMT, G, 1>(a, st) : launch_expert_gemv_nt<FMT, G, 2>(a, st);
+  return a.T <= 5 * std::min(a.E, a.T) || (a.E == 1 && a.T <= 8) ? launch_expert_gemv_nt<FMT, G, 1>(a, st)
+                                                                 : launch_expert_gemv_nt<FMT, G, 2>(a, st);
 }
 
 template <int FMT>
