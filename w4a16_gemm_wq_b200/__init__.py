@@ -287,10 +287,34 @@ def wq_quantize_nvfp4(W: torch.Tensor, scale_s=None) -> PackedNVFP4:
     return PackedNVFP4(codes, bscale, g, N, K)
 
 
-def _same_device(t0: torch.Tensor, *ts):
-    for t in ts:
-        if t is not None and t.device != t0.device:
-            raise ValueError(f"tensors on {t0.device} and {t.device}: all must be on one device")
+def _device_of(*ts) -> int:
+    """Index of the GPU that holds all the given tensors (None among them is skipped)."""
+    index = ts[0].get_device()
+    for t in ts[1:]:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {ts[0].device} and {t.device}: all must be on one device")
+    return index
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object (about 3 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, index: int, *args):
+    """Call an entry point on the current stream of GPU `index`, whichever device is current."""
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != WQ_OK:
+        _check(status, name)
 
 
 def wq_quantize_mxfp4(W: torch.Tensor, scale_s=None) -> PackedMXFP4:
@@ -303,12 +327,9 @@ def wq_quantize_mxfp4(W: torch.Tensor, scale_s=None) -> PackedMXFP4:
         raise ValueError("W must be [N, K]")
     N, K = W.shape
     s = _opt_f32(scale_s, "scale_s", K)
-    _same_device(W, s)
-    with torch.cuda.device(W.device):
-        codes = torch.empty((N, max(K // 2, 1)), dtype=torch.uint8, device=W.device)
-        bscale = torch.empty((N, max(K // 32, 1)), dtype=torch.uint8, device=W.device)
-        _check(load().wq_quantize_mxfp4(_ptr(W), N, K, _ptr(s), _ptr(codes), _ptr(bscale), _stream()),
-               "wq_quantize_mxfp4")
+    codes = W.new_empty((N, max(K // 2, 1)), dtype=torch.uint8)
+    bscale = W.new_empty((N, max(K // 32, 1)), dtype=torch.uint8)
+    _call("wq_quantize_mxfp4", _device_of(W, s), W.data_ptr(), N, K, _addr(s), codes.data_ptr(), bscale.data_ptr())
     return PackedMXFP4(codes, bscale, N, K)
 
 
@@ -323,13 +344,10 @@ def _mx_pack(p: PackedMXFP4):
 def wq_dequantize_mxfp4(p: PackedMXFP4, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of an MXFP4 pack, bf16 [N, K] (exact)."""
     _mx_pack(p)
-    dev = p.codes.device
-    W = out if out is not None else torch.empty((p.N, p.K), dtype=torch.bfloat16, device=dev)
+    W = p.codes.new_empty((p.N, p.K), dtype=torch.bfloat16) if out is None else out
     _dev(W, "out", torch.bfloat16, (p.N, p.K))
-    _same_device(p.codes, p.bscale, W)
-    with torch.cuda.device(dev):
-        _check(load().wq_dequantize_mxfp4(_ptr(p.codes), _ptr(p.bscale), p.N, p.K, _ptr(W), _stream()),
-               "wq_dequantize_mxfp4")
+    _call("wq_dequantize_mxfp4", _device_of(p.codes, p.bscale, W), p.codes.data_ptr(), p.bscale.data_ptr(), p.N, p.K,
+          W.data_ptr())
     return W
 
 
@@ -345,20 +363,21 @@ def wq_quantize_experts(W: torch.Tensor, fmt: str = "mxfp4", group_size: int = 6
     E, N, K = W.shape
     if E < 1:
         raise ValueError("need at least one expert")
-    if fmt == "mxfp4":
-        p = wq_quantize_mxfp4(W.view(E * N, K))
-        return PackedExperts(fmt, E, N, K, p.codes.view(E, N, -1), bscale=p.bscale.view(E, N, -1))
-    if fmt == "int4":
-        p = wq_quantize_int4(W.view(E * N, K), group_size, zero_point)
-        return PackedExperts(fmt, E, N, K, p.qweight.view(E, N, -1), scales=p.scales.view(E, N, -1),
-                             zeros=None if p.zeros is None else p.zeros.view(E, N, -1), group_size=group_size,
-                             zero_point=zero_point)
-    if fmt == "nvfp4":
+    if fmt not in ("int4", "nvfp4", "mxfp4"):
+        raise ValueError(f"unknown format {fmt!r}: int4, nvfp4 or mxfp4")
+    with torch.cuda.device(W.device):
+        if fmt == "mxfp4":
+            p = wq_quantize_mxfp4(W.view(E * N, K))
+            return PackedExperts(fmt, E, N, K, p.codes.view(E, N, -1), bscale=p.bscale.view(E, N, -1))
+        if fmt == "int4":
+            p = wq_quantize_int4(W.view(E * N, K), group_size, zero_point)
+            return PackedExperts(fmt, E, N, K, p.qweight.view(E, N, -1), scales=p.scales.view(E, N, -1),
+                                 zeros=None if p.zeros is None else p.zeros.view(E, N, -1), group_size=group_size,
+                                 zero_point=zero_point)
         ps = [wq_quantize_nvfp4(W[e]) for e in range(E)]
         return PackedExperts(fmt, E, N, K, torch.stack([p.codes for p in ps]),
                              bscale=torch.stack([p.bscale for p in ps]),
                              global_scale=torch.cat([p.global_scale for p in ps]))
-    raise ValueError(f"unknown format {fmt!r}: int4, nvfp4 or mxfp4")
 
 
 def awq_search_scale(W: torch.Tensor, alphas: torch.Tensor, group_size: int = 64, X: torch.Tensor | None = None,
@@ -575,16 +594,14 @@ def wq_linear_mxfp4(X: torch.Tensor, p: PackedMXFP4, act_fp4: int = 0, act_inv_s
     if X.dim() != 2 or X.shape[1] != p.K:
         raise ValueError(f"X must be [M, {p.K}], got {tuple(X.shape)}")
     M, K = X.shape
-    Y = out if out is not None else torch.empty((M, p.N), dtype=torch.bfloat16, device=X.device)
+    Y = X.new_empty((M, p.N)) if out is None else out
     _dev(Y, "out", torch.bfloat16, (M, p.N))
     s = _opt_f32(act_inv_s, "act_inv_s", K)
-    _same_device(X, p.codes, p.bscale, Y, s, ws)
-    with torch.cuda.device(X.device):
-        if ws is None:
-            ws = _workspace(linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4), X.device)
-        _check(load().wq_linear_mxfp4(_ptr(X), M, p.N, K, _ptr(p.codes), _ptr(p.bscale), act_fp4, _ptr(s), _ptr(Y),
-                                      _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream()),
-               "wq_linear_mxfp4")
+    if ws is None and act_fp4:
+        ws = X.new_empty(linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4), dtype=torch.uint8)
+    _call("wq_linear_mxfp4", _device_of(X, p.codes, p.bscale, Y, s, ws), X.data_ptr(), M, p.N, K, p.codes.data_ptr(),
+          p.bscale.data_ptr(), act_fp4, _addr(s), Y.data_ptr(), _addr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
     return Y
 
 
@@ -597,34 +614,26 @@ class ExpertStack(ctypes.Structure):
                 ("global_scale", ctypes.c_void_p)]
 
 
-def _expert_stack(p: PackedExperts) -> ExpertStack:
-    """The wq_expert_stack of a pack, its tensors checked."""
+def _expert_stack(p: PackedExperts):
+    """The wq_expert_stack of a pack, its tensors checked, and their GPU."""
     if not isinstance(p, PackedExperts):
         raise ValueError("need a PackedExperts")
     E, N, K = p.E, p.N, p.K
-    w = ExpertStack(E=E, N=N, K=K)
     if p.fmt == "int4":
         _dev(p.packed, "packed", torch.int32, (E, N, K // 8))
         ng = K // p.group_size if p.group_size in (32, 64, 128) else 1
         _dev(p.scales, "scales", torch.float16, (E, N, ng))
-        if p.zero_point:
-            _dev(p.zeros, "zeros", torch.int32, (E, N, (ng + 7) // 8))
-            w.zeros = p.zeros.data_ptr()
-        w.format, w.scales, w.group_size, w.zero_point = WQ_FMT_INT4, p.scales.data_ptr(), p.group_size, p.zero_point
-        _same_device(p.packed, p.scales, p.zeros)
-    elif p.fmt in ("nvfp4", "mxfp4"):
-        block = 16 if p.fmt == "nvfp4" else 32
-        _dev(p.packed, "packed", torch.uint8, (E, N, K // 2))
-        _dev(p.bscale, "bscale", torch.uint8, (E, N, K // block))
-        w.format, w.bscale = WQ_FMT_MXFP4, p.bscale.data_ptr()
-        if p.fmt == "nvfp4":
-            _dev(p.global_scale, "global_scale", torch.float32, (E,))
-            w.format, w.global_scale = WQ_FMT_NVFP4, p.global_scale.data_ptr()
-        _same_device(p.packed, p.bscale, p.global_scale)
-    else:
+        zeros = _dev(p.zeros, "zeros", torch.int32, (E, N, (ng + 7) // 8)) if p.zero_point else None
+        return ExpertStack(WQ_FMT_INT4, E, N, K, p.packed.data_ptr(), p.scales.data_ptr(), _addr(zeros), p.group_size,
+                           p.zero_point), _device_of(p.packed, p.scales, zeros)
+    if p.fmt not in ("nvfp4", "mxfp4"):
         raise ValueError(f"unknown format {p.fmt!r}: int4, nvfp4 or mxfp4")
-    w.packed = p.packed.data_ptr()
-    return w
+    nv = p.fmt == "nvfp4"
+    _dev(p.packed, "packed", torch.uint8, (E, N, K // 2))
+    _dev(p.bscale, "bscale", torch.uint8, (E, N, K // (16 if nv else 32)))
+    gs = _dev(p.global_scale, "global_scale", torch.float32, (E,)) if nv else None
+    return ExpertStack(WQ_FMT_NVFP4 if nv else WQ_FMT_MXFP4, E, N, K, p.packed.data_ptr(), None, None, 0, 0,
+                       p.bscale.data_ptr(), _addr(gs)), _device_of(p.packed, p.bscale, gs)
 
 
 def wq_linear_experts(X: torch.Tensor, offsets: torch.Tensor, p: PackedExperts,
@@ -633,18 +642,17 @@ def wq_linear_experts(X: torch.Tensor, offsets: torch.Tensor, p: PackedExperts,
     mixture of experts, rows of X (bf16 [T, K]) sorted by expert, offsets int32 [E + 1] on the
     device.  Rows outside [offsets[0], offsets[E]) are left as they are in `out`, and are zero
     in a new result."""
-    w = _expert_stack(p)
+    w, index = _expert_stack(p)
     _dev(X, "X", torch.bfloat16)
     if X.dim() != 2 or X.shape[1] != p.K:
         raise ValueError(f"X must be [T, {p.K}], got {tuple(X.shape)}")
     T = X.shape[0]
     _dev(offsets, "offsets", torch.int32, (p.E + 1,))
-    Y = out if out is not None else torch.zeros((T, p.N), dtype=torch.bfloat16, device=X.device)
+    Y = X.new_zeros((T, p.N)) if out is None else out
     _dev(Y, "out", torch.bfloat16, (T, p.N))
-    _same_device(X, offsets, p.packed, Y)
-    with torch.cuda.device(X.device):
-        _check(load().wq_linear_experts(ctypes.byref(w), _ptr(X), T, _ptr(offsets), _ptr(Y), _stream()),
-               "wq_linear_experts")
+    if _device_of(X, offsets, Y) != index:
+        raise ValueError("X and the weights must be on one device")
+    _call("wq_linear_experts", index, ctypes.byref(w), X.data_ptr(), T, offsets.data_ptr(), Y.data_ptr())
     return Y
 
 
