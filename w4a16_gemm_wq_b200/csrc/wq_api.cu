@@ -17,6 +17,7 @@
 #include "awq.cuh"
 #include "experts.cuh"
 #include "gemm_fp4.cuh"
+#include "gemm_mxf4.cuh"
 #include "gemm_tcgen05.cuh"
 #include "gemv.cuh"
 #include "gemv_mma.cuh"
@@ -526,14 +527,13 @@ int launch_fp4_bn(wq::Fp4Args& a, const uint8_t* xcodes, const uint8_t* wcodes, 
 // ---------------------------------------------------------------- MXFP4
 // Workspace of the MXFP4 W4A4 path: X as MXFP4 (codes [M, K/2], E8M0 scales [M, K/32]).
 struct MxA4Layout {
-  size_t off_codes, off_sf, off_x, total;
+  size_t off_codes, off_sf, total;
 };
 MxA4Layout mx_a4_layout(int64_t M, int64_t K) {
   MxA4Layout L = {};
   L.off_codes = 0;
   L.off_sf = align256(size_t(M) * size_t(K / 2));
-  L.off_x = align256(L.off_sf + size_t(M) * size_t(K / 32));
-  L.total = align256(L.off_x + size_t(M) * size_t(K) * 2);
+  L.total = align256(L.off_sf + size_t(M) * size_t(K / 32));
   return L;
 }
 
@@ -572,6 +572,28 @@ int mxfp4_unpack_launch(const uint8_t* codes, const uint8_t* bscale, int64_t R, 
   const uint64_t words = uint64_t(R) * uint64_t(C / 8);
   return launch_pdl(wq::mxfp4_unpack_kernel, dim3(mx_grid(words)), dim3(wq::kMxThreads), 0, st, "mxfp4_unpack launch",
                     reinterpret_cast<const uint32_t*>(codes), bscale, words, out);
+}
+
+// MXFP4 W4A4: one CTA per SM over 128 x 192 tiles.
+int launch_mxf4(wq::Mxf4Args& a, const uint8_t* xcodes, const uint8_t* wcodes, cudaStream_t st) {
+  using S = wq::Mxf4Shape;
+  if (int e = make_tmap_2d(&a.tmA, xcodes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.M), uint64_t(a.K / 2),
+                           wq::kGemmBM, wq::kFp4BK / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  if (int e = make_tmap_2d(&a.tmB, wcodes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.N), uint64_t(a.K / 2), S::BN,
+                           wq::kFp4BK / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  a.y_tma = (a.N % 8 == 0) && aligned16(a.Y);
+  if (a.y_tma) {
+    if (int e = make_tmap_2d(&a.tmY, a.Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(a.M), uint64_t(a.N), 32, 32,
+                             CU_TENSOR_MAP_SWIZZLE_64B))
+      return e;
+  }
+  static std::atomic<uint64_t> attr_done{0};
+  if (int e = ensure_smem_attr(wq::gemm_mxf4_kernel, S::SMEM_BYTES, &attr_done, "mxf4 smem attribute")) return e;
+  const int64_t tiles = int64_t((a.N + S::BN - 1) / S::BN) * ((a.M + wq::kGemmBM - 1) / wq::kGemmBM);
+  return launch_pdl(wq::gemm_mxf4_kernel, dim3(unsigned(std::min<int64_t>(tiles, wq::kTcMaxCtas))), dim3(S::THREADS),
+                    S::SMEM_BYTES, st, "mxf4 gemm launch", a);
 }
 
 // ---------------------------------------------------------------- experts
@@ -1622,10 +1644,10 @@ int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
     REQUIRE_PTR(ws);
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     if (int e = mxfp4_pack_launch(X, M, K, act_inv_s, wsb + L.off_codes, wsb + L.off_sf, st)) return e;
-    uint16_t* xv = reinterpret_cast<uint16_t*>(wsb + L.off_x);
-    if (int e = mxfp4_unpack_launch(wsb + L.off_codes, wsb + L.off_sf, M, K, xv, st)) return e;
-    X = xv;
-    a.inv_s = nullptr;
+    wq::Mxf4Args f = {};
+    f.sfa = wsb + L.off_sf; f.sfb = bscale; f.Y = Y;
+    f.M = int(M); f.N = int(N); f.K = int(K);
+    return launch_mxf4(f, wsb + L.off_codes, codes, st);
   }
   return launch_experts(a, WQ_FMT_MXFP4, X, codes, st);
 }
