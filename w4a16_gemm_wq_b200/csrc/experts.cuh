@@ -741,102 +741,149 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: mma.sync with the weights (16 rows of W_e) as the A operand,
-// dequantized in registers, and up to 8 NT rows of X as B.  Bound by HBM (0.53 to
-// 0.63 bytes a weight) and by the dequantization's instructions, both within 20%.
+// dequantized in registers, and up to 8 NT rows of X as B, both in fp16.  Bound by HBM
+// (0.53 to 0.63 bytes a weight) and by the instructions of the dequantization, which
+// is why both operands are fp16: a pair of E2M1 codes is one conversion and one product
+// there, against one conversion, two multiply-adds and a packing in bf16.
 //
-// A unit is 16 weight rows of one row tile; its steps are 128 k each.  A CTA takes a
-// contiguous share of the units, its warps contiguous shares of the CTA's steps, so that
-// every SM streams the same number of bytes whatever K is, and only units that
-// straddle warps are summed through shared memory, in warp order.  A step's codes come
-// by cp.async, kVecDepth steps ahead, into slots that the copying lane reads itself
-// (no barrier, and a loop body of one step: the kernel is short, and a body unrolled
-// over the steps in flight spent most of it on instruction fetches); scales and a
-// word's rows of X one step ahead into registers (L2 holds the scales' sector from the
-// first step that touched it, L1 the rows that all warps of a CTA read).
-// Lane (g, c) (g = lane / 4, c = lane % 4) holds codes of rows g and g + 8: the k order
-// inside an MMA is free, so its four k of each are four consecutive k of the lane's.
+// A unit is 16 weight rows of one row tile; a step of it is 128 k.  A cluster of
+// `split` CTAs takes a contiguous share of the units, each of its CTAs a share of K (so
+// that a tile's rows fit shared memory), each of a CTA's 16 warps a contiguous share of
+// the CTA's steps: every SM streams the same number of bytes whatever N and K are.
+// Units that straddle warps are summed through shared memory, in warp order, and
+// the CTAs of a cluster through distributed shared memory, in rank order.
+//
+// X is staged once per row tile in the order of the MMA's B fragments, each row scaled
+// by a power of two that puts its largest finite magnitude at 2^14: fp16 then holds
+// bf16 exactly down to 2^-31 of that magnitude, and what is smaller to 2^-39 of it.
+// Codes come by cp.async, kVecDepth - 1 steps ahead, into slots that the copying lane
+// reads itself (no barrier, and a loop body of one step: a body unrolled over the steps
+// in flight spent the short kernel's time on instruction fetches); scales one step
+// ahead into registers.
+// Lane (g, c) (g = lane / 4, c = lane % 4) holds codes of rows g and g + 8; the k order
+// inside an MMA is free, so its four k of each are four of the lane's own:
 //   INT4   lane c takes G / 4 k of every group, so that an MMA stays inside a group: A is
-//          q - z (exact in bf16), and the fp16 scale multiplies the group's fp32 sums;
-//   E2M1   lane c takes 32 k in a row; A is the code times its block scale, exact in bf16.
+//          q - z or 16 (q - z) (exact; X of the latter staged / 16), and the fp16 scale
+//          multiplies the group's fp32 sums;
+//   NVFP4  lane c takes 32 k in a row; A is the code times its block scale (exact);
+//   MXFP4  the same, with the block scale relative to the largest of the row's step, and
+//          the step's fp32 sums times that one; blocks under 2^-26 of it take another turn.
 constexpr int kVecWarps = 16;
 constexpr int kVecDepth = 4;
-constexpr int kVecSmem = kVecWarps * kVecDepth * 1024;
+constexpr int kVecRing = kVecWarps * kVecDepth * 1024;
 
-// FULL: K % 128 == 0, no step reaches past K (and scale bytes of a step are aligned words).
+// Shared memory: codes [warp][kVecDepth][2][32 lanes][16 bytes], the CTA's sums of a run of units
+// (where a cluster shares them), sums of units that straddle warps, X fragments.
+template <int NT>
+struct VecShape {
+  static constexpr int SUM_BYTES = 16 * 8 * NT * 4;              // one unit's sums
+  static constexpr int MAX_UNITS = 16;
+  static constexpr int OFF_SUMS = kVecRing;
+  static constexpr int OFF_PART = OFF_SUMS + MAX_UNITS * SUM_BYTES;
+  static constexpr int OFF_X = OFF_PART + 2 * kVecWarps * SUM_BYTES;
+  static constexpr int STEP_BYTES = NT * 2048;                   // X fragments of a step
+  static constexpr int MAX_STEPS = (216 * 1024 - OFF_X) / STEP_BYTES;
+};
+
 __device__ __forceinline__ uint32_t ldg_u16(const void* p) { return __ldg(static_cast<const uint16_t*>(p)); }
 __device__ __forceinline__ uint32_t ldg_u8(const void* p) { return __ldg(static_cast<const uint8_t*>(p)); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
+// FULL: K % 128 == 0, no step reaches past K (and a step's scales of a row are aligned words).
 template <int FMT, int G, int NT, bool FULL>
 __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __grid_constant__ ExpertArgs a) {
   static_assert(FMT != GEMM_INT4 || G == 32 || G == 64 || G == 128, "group size");
+  using V = VecShape<NT>;
   constexpr int NG = FMT == GEMM_INT4 ? 128 / G : 1;    // groups of a step
   constexpr int WPG = 4 / NG;                           // words (8 k) of a lane per group
+  extern __shared__ __align__(1024) uint8_t vec_smem[];
   __shared__ int bound[kMaxExperts + 4], tstart[kMaxExperts + 4];
   __shared__ int bad_flag;
-  __shared__ float part[2 * kVecWarps][16][8 * NT];     // sums of units that straddle warps
-  extern __shared__ __align__(16) uint8_t vec_smem[];   // codes: [warp][kVecDepth][2][32 lanes][16 bytes]
+  __shared__ uint32_t rtop[8 * NT];                     // largest finite magnitude of X's rows, fp32 bits
+  __shared__ float rscale[8 * NT];                      // what undoes their scaling
+  float (*part)[16][8 * NT] = reinterpret_cast<float (*)[16][8 * NT]>(vec_smem + V::OFF_PART);
+  float (*sums)[16][8 * NT] = reinterpret_cast<float (*)[16][8 * NT]>(vec_smem + V::OFF_SUMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int K = a.K, N = a.N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 0) expert_tables(a, 8 * NT, bound, tstart, &bad_flag);
-  __syncthreads();
-  if (bad_flag) return;
-  const int nrb = (N + 15) >> 4, S = (K + 127) >> 7;  // row blocks of an expert, steps of a unit
-  // the CTA's units and the warps' first steps of them
-  const int units = tstart[a.E] * nrb, per = units / gridDim.x, more = units - per * gridDim.x;
-  const int u0 = blockIdx.x * per + min(int(blockIdx.x), more), nu = per + (int(blockIdx.x) < more);
-  const int tot = nu * S;
-  const auto first_of = [&](int w) { return int(int64_t(tot) * w / kVecWarps); };
+  if (a.offsets) {
+    if (warp == 0) expert_tables(a, 8 * NT, bound, tstart, &bad_flag);
+    __syncthreads();
+    if (bad_flag) return;
+  }
+  const int tiles = a.offsets ? tstart[a.E] : (a.T + 8 * NT - 1) / (8 * NT);
+  const int nrb = (N + 15) >> 4;                        // row blocks of an expert
+  // this cluster's units, this CTA's steps of each
+  int rank = 0, cl = blockIdx.x, ncl = gridDim.x, S0 = 0, S = (K + 127) >> 7;
+  if (a.split > 1) {
+    rank = int(cluster_ctarank());
+    cl /= a.split;
+    ncl /= a.split;
+    const int all = S;
+    S0 = all * rank / a.split;
+    S = all * (rank + 1) / a.split - S0;
+  }
+  const int units = tiles * nrb, per = units / ncl, more = units - per * ncl;
+  int u0 = cl * per + min(cl, more);
+  const int ulast = u0 + per + (cl < more);
 
-  struct Unit {
-    int e, row, rows, n0;
-  };
-  const auto unit_of = [&](int u) {
-    Unit t;
-    const int tile = u / nrb;
-    t.n0 = (u - tile * nrb) * 16;
-    t.e = expert_of_tile(tstart, a.E, tile);
-    const int r = bound[t.e + 1] - bound[t.e], nt = tstart[t.e + 1] - tstart[t.e];
-    const int w = (r + nt - 1) / nt;  // the expert's rows, evenly over its tiles
-    t.row = bound[t.e] + (tile - tstart[t.e]) * w;
-    t.rows = min(w, bound[t.e + 1] - t.row);
-    return t;
-  };
-  // k of word j (8 codes) of this lane within a step
-  const auto k_of = [&](int j) { return FMT == GEMM_INT4 ? (j / WPG) * G + c * (G / 4) + (j % WPG) * 8 : 32 * c + 8 * j; };
   const int zw = (((FMT == GEMM_INT4 ? K / G : 8) + 7) >> 3) * 4;  // zero-point bytes of a row
   const int sw = FMT == GEMM_INT4 ? K / G * 2 : FMT == GEMM_NVFP4 ? K >> 4 : K >> 5;  // scale bytes of a row
-  const uint8_t* sbase = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
-
+  constexpr int SB = FMT == GEMM_INT4 ? 2 * NG : FMT == GEMM_NVFP4 ? 8 : 4;           // of a step
+  const uint8_t* scales = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
   const uint32_t ring = smem_u32(vec_smem) + uint32_t(warp * kVecDepth * 1024 + lane * 16);
-  int at = first_of(warp);
-  const int end = first_of(warp + 1);
-  while (at < end) {
-    // ---- the warp's steps [ja, jb) of a unit
-    const int u = at / S, ja = at - u * S, jb = min(S, ja + end - at);
-    at += jb - ja;
-    const Unit t = unit_of(u0 + u);
-    const int64_t rlo = int64_t(t.e) * N + min(t.n0 + g, N - 1), rhi = int64_t(t.e) * N + min(t.n0 + g + 8, N - 1);
-    // cursors: codes kVecDepth - 1 steps ahead, scales and X one step ahead
-    const uint8_t* plo = a.packed + rlo * (K >> 1) + ja * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
-    const uint8_t* phi = plo + (rhi - rlo) * (K >> 1);
-    constexpr int SB = FMT == GEMM_INT4 ? 2 * NG : FMT == GEMM_NVFP4 ? 8 : 4;  // scale bytes of a step
-    const uint8_t* slo = sbase + rlo * sw + ja * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
-    const uint8_t* shi = slo + (rhi - rlo) * sw;
-    const uint8_t* zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
-    const uint8_t* zhi = zlo + (rhi - rlo) * zw;
-    const uint16_t* xp[NT];  // this lane's rows of X; a lane without one reads the tile's last (its sums are not stored)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      xp[n] = a.X + int64_t(t.row + min(8 * n + g, t.rows - 1)) * K + ja * 128 + (FMT == GEMM_INT4 ? c * (G / 4) : 32 * c);
+  const uint32_t xfrag = smem_u32(vec_smem) + uint32_t(V::OFF_X + lane * 16);
+  int staged = -1;  // tile whose rows are in shared memory
 
+  while (u0 < ulast) {
+    // ---- a run of units of one row tile
+    const int tile = u0 / nrb;
+    int u1 = min(ulast, (tile + 1) * nrb);
+    if (a.split > 1) u1 = min(u1, u0 + V::MAX_UNITS);
+    int e = 0, row = tile * 8 * NT, rows = min(8 * NT, a.T - row);
+    if (a.offsets) {
+      e = expert_of_tile(tstart, a.E, tile);
+      const int r = bound[e + 1] - bound[e], nt = tstart[e + 1] - tstart[e];
+      const int w = (r + nt - 1) / nt;  // the expert's rows, evenly over its tiles
+      row = bound[e] + (tile - tstart[e]) * w;
+      rows = min(w, bound[e + 1] - row);
+    }
+    const int nb0 = (u0 - tile * nrb) * 16, tot = (u1 - u0) * S;  // first weight row; steps of the CTA
+    const auto first_of = [&](int w) { return int(int64_t(tot) * w / kVecWarps); };
+    const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + e) : 1.f;
+    int at = first_of(warp);
+    const int end = first_of(warp + 1);
+
+    // ---- cursors of a unit's steps: codes kVecDepth - 1 steps ahead, scales one step ahead
+    const uint8_t *plo, *phi, *slo, *shi, *zlo, *zhi;
+    uint32_t put, take;
+    const auto open = [&](int u, int j) {  // at step j of unit u
+      const int64_t rlo = int64_t(e) * N + min(nb0 + u * 16 + g, N - 1);
+      const int64_t d = int64_t(e) * N + min(nb0 + u * 16 + g + 8, N - 1) - rlo;
+      plo = a.packed + rlo * (K >> 1) + (S0 + j) * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
+      phi = plo + d * (K >> 1);
+      slo = scales + rlo * sw + (S0 + j) * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
+      shi = slo + d * sw;
+      zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
+      zhi = zlo + d * zw;
+      put = take = ring;
+    };
     // a lane's 16 code bytes of each row, in word order; zeros past K
-    uint32_t put = ring + uint32_t(ja % kVecDepth) * 1024u;
     const auto request = [&](int j) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const bool in = FULL || (FMT == GEMM_INT4 ? j * 128 + i * G < K : j * 128 + 32 * c < K);
+        const int k0 = (S0 + j) * 128;
+        const bool in = FULL || (FMT == GEMM_INT4 ? k0 + i * G < K : k0 + 32 * c < K);
         cp_async_zfill<16 / NG>(put + i * (16 / NG), in ? plo + i * (G / 2) : a.packed, in ? 16 / NG : 0);
         cp_async_zfill<16 / NG>(put + 512 + i * (16 / NG), in ? phi + i * (G / 2) : a.packed, in ? 16 / NG : 0);
       }
@@ -844,177 +891,291 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       phi += 64;
       put = put + 1024u == ring + kVecDepth * 1024u ? ring : put + 1024u;
     };
-    // scales, row g's in the low half (fp16 per group, two E4M3 bytes, or an E8M0 byte), and
-    // the bytes that hold the step's zero points (one for G >= 64, else two)
-    uint32_t sc[NG], zp = 0x88888888u;
+    const auto fill = [&](int j0, int j1) {
+#pragma unroll 1
+      for (int i = 0; i < kVecDepth - 1; ++i) {
+        if (j0 + i < j1) request(j0 + i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+    };
+    // scales of rows g and g + 8 (fp16 per group, two E4M3 bytes, or an E8M0 byte) and the bytes
+    // that hold the step's zero points (one for G >= 64, else two), as they are loaded: nothing
+    // waits for them before the step that uses them
+    uint32_t scl[NG], sch[NG], zpl = 0x8888u, zph = 0x8888u;
     const auto load_scales = [&](int j) {
       if (FMT == GEMM_INT4 && FULL && NG > 1) {  // a row's scales of the step as words
 #pragma unroll
         for (int i = 0; i < NG; i += 2) {
-          const uint32_t l = __ldg(reinterpret_cast<const uint32_t*>(slo + 2 * i));
-          const uint32_t h = __ldg(reinterpret_cast<const uint32_t*>(shi + 2 * i));
-          sc[i] = prmt_b32(l, h, 0x5410);
-          sc[(i + 1) % NG] = prmt_b32(l, h, 0x7632);
+          scl[i] = __ldg(reinterpret_cast<const uint32_t*>(slo + 2 * i));
+          sch[i] = __ldg(reinterpret_cast<const uint32_t*>(shi + 2 * i));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          const bool in = FULL || (FMT == GEMM_INT4 ? (j * NG + i) * 2 < sw : j * 128 + 32 * c < K);
-          sc[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) | (ldg_u8(shi) << 16)
-                                               : ldg_u16(slo + 2 * i) | (ldg_u16(shi + 2 * i) << 16);
+          const bool in = FULL || (FMT == GEMM_INT4 ? ((S0 + j) * NG + i) * 2 < sw : (S0 + j) * 128 + 32 * c < K);
+          scl[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) : ldg_u16(slo + 2 * i);
+          sch[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(shi) : ldg_u16(shi + 2 * i);
         }
       }
       slo += SB;
       shi += SB;
       if (FMT == GEMM_INT4 && a.zeros) {
-        const int b = (j * NG) >> 1;
-        zp = G == 32 ? ldg_u16(zlo + b) | (ldg_u16(zhi + b) << 16) : ldg_u8(zlo + b) | (ldg_u8(zhi + b) << 16);
+        const int b = ((S0 + j) * NG) >> 1;
+        zpl = G == 32 ? ldg_u16(zlo + b) : ldg_u8(zlo + b);
+        zph = G == 32 ? ldg_u16(zhi + b) : ldg_u8(zhi + b);
       }
-    };
-    const auto xload = [&](int n, int w, int j) {
-      const int k = FMT == GEMM_INT4 ? (w / WPG) * G + (w % WPG) * 8 : 8 * w;  // past the lane's first of the step
-      return FULL || j * 128 + k_of(w) < K ? ldg_v4(xp[n] + k) : make_uint4(0, 0, 0, 0);
     };
 
-    uint4 x[NT][4];
-    float acc[NT][4];
-#pragma unroll 1
-    for (int i = 0; i < kVecDepth - 1; ++i) {
-      if (ja + i < jb) request(ja + i);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    int u = 0, ja = 0;
+    if (at < end) {  // the first codes are under way while X is staged
+      u = at / S;
+      ja = at - u * S;
+      open(u, ja);
+      fill(ja, min(S, ja + end - at));
+      load_scales(ja);
     }
-    load_scales(ja);
-    uint32_t take = ring + uint32_t(ja % kVecDepth) * 1024u;
+    if (staged != tile) {
+      // X, or X * act_inv_s, 256 k of a row at a time: the rows' largest finite magnitudes, then the fragments
+      if (threadIdx.x < 8 * NT) rtop[threadIdx.x] = 0;
+      __syncthreads();  // also: the last run's readers are done
+      const float* f = FMT == GEMM_MXFP4 && a.inv_s ? a.inv_s + S0 * 128 : nullptr;
+      const int len = min(S * 128, K - S0 * 128), pieces = (S + 1) >> 1;
+      const auto load8 = [&](int m, int k, float (&v)[8]) {
+        if (k >= len) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+          for (int j = 0; j < 8; ++j) v[j] = 0.f;
+          return;
+        }
+        const uint4 r = ldg_v4(a.X + int64_t(row + m) * K + S0 * 128 + k);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) x[n][w] = xload(n, w, ja);
-      xp[n] += 128;
-      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    }
-#pragma unroll 1
-    for (int j = ja; j < jb; ++j) {
-      if (j + kVecDepth - 1 < jb) request(j + kVecDepth - 1);
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kVecDepth - 1) : "memory");
-      const uint4 cl = ld_shared_v4(take), ch = ld_shared_v4(take + 512);
-      take = take + 1024u == ring + kVecDepth * 1024u ? ring : take + 1024u;
-      const uint32_t wl[4] = {cl.x, cl.y, cl.z, cl.w}, wh[4] = {ch.x, ch.y, ch.z, ch.w};
-      uint32_t s[NG];
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+        if (f) {
+          const float4 f0 = __ldg(reinterpret_cast<const float4*>(f + k)), f1 = __ldg(reinterpret_cast<const float4*>(f + k) + 1);
+          v[0] *= f0.x; v[1] *= f0.y; v[2] *= f0.z; v[3] *= f0.w;
+          v[4] *= f1.x; v[5] *= f1.y; v[6] *= f1.z; v[7] *= f1.w;
+        }
+      };
+#pragma unroll 2
+      for (int i = warp; i < rows * pieces; i += kVecWarps) {
+        const int m = i / pieces, k = (i - m * pieces) * 256 + lane * 8;
+        float v[8];
+        load8(m, k, v);
+        uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) s[i] = sc[i];
-      const uint32_t z = zp;
-      if (j + 1 < jb) load_scales(j + 1);
-      uint32_t s2lo = 0, s2hi = 0;
-      bool f16 = true;  // MXFP4: the warp's block scales are normal fp16 values
-      if (FMT == GEMM_NVFP4) {
-        s2lo = tc_e4m3x2(s[0] & 0x7F7Fu);
-        s2hi = tc_e4m3x2((s[0] >> 16) & 0x7F7Fu);
-      } else if (FMT == GEMM_MXFP4) {
-        const uint32_t el = s[0] & 255u, eh = s[0] >> 16;
-        f16 = __all_sync(0xffffffffu, el - 113u < 30u && eh - 113u < 30u);
-        s2lo = f16 ? (el - 112u) << 10 : __float_as_uint(e8m0_f32(el));
-        s2hi = f16 ? (eh - 112u) << 10 : __float_as_uint(e8m0_f32(eh));
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+          top = max(top, b < 0x7F800000u ? b : 0u);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(&rtop[m], top);
       }
-      float d[NT][4];  // INT4: the group's sums
+      __syncthreads();
+#pragma unroll 2
+      for (int i = warp; i < rows * pieces; i += kVecWarps) {
+        const int m = i / pieces, k = (i - m * pieces) * 256 + lane * 8;
+        const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
+        const float up = __uint_as_float(fe << 23);
+        if (lane == 0 && k == 0) rscale[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
+        if (k >= S * 128) continue;  // an odd number of steps
+        float v[8];
+        load8(m, k, v);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t al[4], ah[4];
-        if (FMT == GEMM_INT4) {
-          const int nib = 4 * ((G == 128 ? (j & 1) : 0) + w / WPG);  // this group's zero point
-          const uint32_t zl = 0x43004300u + ((z >> nib) & 15u) * 0x00010001u;
-          const uint32_t zh = 0x43004300u + ((z >> (16 + nib)) & 15u) * 0x00010001u;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {  // {code q, code q + 4}
-            al[q] = bf16x2_sub(lop3_andor(wl[w] >> (4 * q), 0x000F000Fu, 0x43004300u), zl);
-            ah[q] = bf16x2_sub(lop3_andor(wh[w] >> (4 * q), 0x000F000Fu, 0x43004300u), zh);
-          }
-        } else if (FMT == GEMM_NVFP4) {
-          if (w < 2) {
-            dequant8_e2m1<0>(wl[w], s2lo, al);
-            dequant8_e2m1<0>(wh[w], s2hi, ah);
-          } else {
-            dequant8_e2m1<1>(wl[w], s2lo, al);
-            dequant8_e2m1<1>(wh[w], s2hi, ah);
-          }
-        } else if (f16) {
-          dequant8_e2m1<0>(wl[w], s2lo, al);
-          dequant8_e2m1<0>(wh[w], s2hi, ah);
+        for (int j = 0; j < 8; ++j) v[j] *= up;
+        const int p = (k & 127) >> 3;  // 8-k piece of the step: word w of lane cc
+        uint4 o;
+        int w, cc;
+        if constexpr (FMT == GEMM_INT4) {
+          // {code i, code i + 4} of a word: x0 x4 | x1 x5 (of 16 q) | x2 x6 | x3 x7 (of 16 q)
+          cc = (p * 8 % G) / (G / 4);
+          w = (p * 8 / G) * WPG + (p * 8 % (G / 4)) / 8;
+          o = make_uint4(pack_f16x2(v[0], v[4]), pack_f16x2(v[1] * 0.0625f, v[5] * 0.0625f), pack_f16x2(v[2], v[6]),
+                         pack_f16x2(v[3] * 0.0625f, v[7] * 0.0625f));
         } else {
-          dequant8_e2m1_f32(wl[w], __uint_as_float(s2lo), nullptr, al);
-          dequant8_e2m1_f32(wh[w], __uint_as_float(s2hi), nullptr, ah);
+          cc = p >> 2;
+          w = p & 3;
+          o = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
         }
+        st_shared_v4(smem_u32(vec_smem) + uint32_t(V::OFF_X + (k >> 7) * V::STEP_BYTES + (m >> 3) * 2048 + w * 512 +
+                                                   (4 * (m & 7) + cc) * 16), o);
+      }
+      staged = tile;
+      __syncthreads();
+    }
+
+    // ---- the warp's steps, unit by unit
+    while (at < end) {
+      const int jb = min(S, ja + end - at);
+      float acc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint4 b = x[n][w];
-          if (j + 1 < jb) x[n][w] = xload(n, w, j + 1);
-          const int k = j * 128 + k_of(w);
-          if (FMT == GEMM_MXFP4 && a.inv_s && k < K) {  // X * act_inv_s, rounded to bf16 once
-            const float4 i0 = __ldg(reinterpret_cast<const float4*>(a.inv_s + k));
-            const float4 i1 = __ldg(reinterpret_cast<const float4*>(a.inv_s + k) + 1);
-            b.x = pack_bf16x2(__uint_as_float(b.x << 16) * i0.x, __uint_as_float(b.x & 0xFFFF0000u) * i0.y);
-            b.y = pack_bf16x2(__uint_as_float(b.y << 16) * i0.z, __uint_as_float(b.y & 0xFFFF0000u) * i0.w);
-            b.z = pack_bf16x2(__uint_as_float(b.z << 16) * i1.x, __uint_as_float(b.z & 0xFFFF0000u) * i1.y);
-            b.w = pack_bf16x2(__uint_as_float(b.w << 16) * i1.z, __uint_as_float(b.w & 0xFFFF0000u) * i1.w);
-          }
-          if (FMT == GEMM_INT4) {
-            if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-            // {x0, x4} {x1, x5} | {x2, x6} {x3, x7}
-            mma_bf16_16816(d[n], al[0], ah[0], al[1], ah[1], prmt_b32(b.x, b.z, 0x5410), prmt_b32(b.x, b.z, 0x7632));
-            mma_bf16_16816(d[n], al[2], ah[2], al[3], ah[3], prmt_b32(b.y, b.w, 0x5410), prmt_b32(b.y, b.w, 0x7632));
-            if (w % WPG == WPG - 1) {
-              const float sl = __half2float(__ushort_as_half(uint16_t(s[w / WPG])));
-              const float sh = __half2float(__ushort_as_half(uint16_t(s[w / WPG] >> 16)));
-              acc[n][0] = fmaf(sl, d[n][0], acc[n][0]);
-              acc[n][1] = fmaf(sl, d[n][1], acc[n][1]);
-              acc[n][2] = fmaf(sh, d[n][2], acc[n][2]);
-              acc[n][3] = fmaf(sh, d[n][3], acc[n][3]);
+      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll 1
+      for (int j = ja; j < jb; ++j) {
+        if (j + kVecDepth - 1 < jb) request(j + kVecDepth - 1);
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kVecDepth - 1) : "memory");
+        const uint4 cl4 = ld_shared_v4(take), ch4 = ld_shared_v4(take + 512);
+        take = take + 1024u == ring + kVecDepth * 1024u ? ring : take + 1024u;
+        const uint32_t wl[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, wh[4] = {ch4.x, ch4.y, ch4.z, ch4.w};
+        uint32_t s[NG];  // row g's in the low half
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const bool words = FMT == GEMM_INT4 && FULL && NG > 1;
+          s[i] = prmt_b32(scl[words ? i & ~1 : i], sch[words ? i & ~1 : i], words && (i & 1) ? 0x7632 : 0x5410);
+        }
+        const uint32_t z = zpl | (zph << 16);
+        if (j + 1 < jb) load_scales(j + 1);
+        const uint32_t xs = xfrag + uint32_t(j * V::STEP_BYTES);
+        if (FMT == GEMM_INT4) {
+          float d[NT][4];  // the group's sums
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int nib = 4 * ((G == 128 ? ((S0 + j) & 1) : 0) + w / WPG);  // this group's zero point
+            const uint32_t zl = ((z >> nib) & 15u) * 0x00010001u, zh = ((z >> (16 + nib)) & 15u) * 0x00010001u;
+            constexpr uint32_t B = 0x64006400u;  // fp16 1024: a code under it is 1024 + q (or + 16 q)
+            const uint32_t zl1 = B + zl, zl16 = B + zl * 16u, zh1 = B + zh, zh16 = B + zh * 16u;
+            const uint32_t l8 = wl[w] >> 8, h8 = wh[w] >> 8;
+            const uint32_t a0 = f16x2_sub(lop3_andor(wl[w], 0x000F000Fu, B), zl1);
+            const uint32_t a1 = f16x2_sub(lop3_andor(wh[w], 0x000F000Fu, B), zh1);
+            const uint32_t a2 = f16x2_sub(lop3_andor(wl[w], 0x00F000F0u, B), zl16);
+            const uint32_t a3 = f16x2_sub(lop3_andor(wh[w], 0x00F000F0u, B), zh16);
+            const uint32_t b0 = f16x2_sub(lop3_andor(l8, 0x000F000Fu, B), zl1);
+            const uint32_t b1 = f16x2_sub(lop3_andor(h8, 0x000F000Fu, B), zh1);
+            const uint32_t b2 = f16x2_sub(lop3_andor(l8, 0x00F000F0u, B), zl16);
+            const uint32_t b3 = f16x2_sub(lop3_andor(h8, 0x00F000F0u, B), zh16);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
+              if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+              mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
+              mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
+              if (w % WPG == WPG - 1) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s[w / WPG]));
+                acc[n][0] = fmaf(f.x, d[n][0], acc[n][0]);
+                acc[n][1] = fmaf(f.x, d[n][1], acc[n][1]);
+                acc[n][2] = fmaf(f.y, d[n][2], acc[n][2]);
+                acc[n][3] = fmaf(f.y, d[n][3], acc[n][3]);
+              }
             }
+          }
+        } else {
+          // A = code times scale; fp16 pairs of the lane's two NVFP4 blocks, or of its MXFP4 block
+          const auto products = [&](uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1, float (&d)[NT][4]) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t sl = w < 2 ? l0 : l1, sh = w < 2 ? h0 : h1;
+              const uint32_t a0 = h2_mul(e2m1x2_of_byte<0>(wl[w]), sl), a2 = h2_mul(e2m1x2_of_byte<1>(wl[w]), sl);
+              const uint32_t b0 = h2_mul(e2m1x2_of_byte<2>(wl[w]), sl), b2 = h2_mul(e2m1x2_of_byte<3>(wl[w]), sl);
+              const uint32_t a1 = h2_mul(e2m1x2_of_byte<0>(wh[w]), sh), a3 = h2_mul(e2m1x2_of_byte<1>(wh[w]), sh);
+              const uint32_t b1 = h2_mul(e2m1x2_of_byte<2>(wh[w]), sh), b3 = h2_mul(e2m1x2_of_byte<3>(wh[w]), sh);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
+                mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
+                mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
+              }
+            }
+          };
+          if (FMT == GEMM_NVFP4) {
+            const uint32_t fl = tc_e4m3x2(s[0] & 0x7F7Fu), fh = tc_e4m3x2((s[0] >> 16) & 0x7F7Fu);
+            products(prmt_b32(fl, fl, 0x1010), prmt_b32(fl, fl, 0x3232), prmt_b32(fh, fh, 0x1010),
+                     prmt_b32(fh, fh, 0x3232), acc);
           } else {
-            mma_bf16_16816(acc[n], al[0], ah[0], al[1], ah[1], b.x, b.y);
-            mma_bf16_16816(acc[n], al[2], ah[2], al[3], ah[3], b.z, b.w);
+            // a block whose codes are all zero counts for none (a NaN scale does)
+            uint32_t rest = s[0];  // scale bytes of the blocks still to be taken, + 1, row g's in the low half
+            {
+              const uint32_t el = s[0] & 0xFFFFu, eh = s[0] >> 16;
+              const bool zl = ((wl[0] | wl[1] | wl[2] | wl[3]) & 0x77777777u) == 0 && el != 255u;
+              const bool zh = ((wh[0] | wh[1] | wh[2] | wh[3]) & 0x77777777u) == 0 && eh != 255u;
+              rest = (zl ? 0u : el + 1u) | (zh ? 0u : (eh + 1u) << 16);
+            }
+#pragma unroll 1
+            while (__any_sync(0xffffffffu, rest != 0)) {
+              // the rows' largest scales among them, and the blocks within 2^-26 of those
+              uint32_t top = max_u16x2(rest, __shfl_xor_sync(0xffffffffu, rest, 1));
+              top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const uint32_t tl = top & 0xFFFFu, th = top >> 16, rl = rest & 0xFFFFu, rh = rest >> 16;
+              const bool inl = rl != 0 && rl + 26u >= tl, inh = rh != 0 && rh + 26u >= th;
+              // fp16 2^(13 + e - top): exponent field 28 + e - top
+              const uint32_t fl = !inl ? 0u : rl == 256u ? 0x7E00u : (28u + rl - tl) << 10;
+              const uint32_t fh = !inh ? 0u : rh == 256u ? 0x7E00u : (28u + rh - th) << 10;
+              float d[NT][4];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+              products(fl * 0x10001u, fl * 0x10001u, fh * 0x10001u, fh * 0x10001u, d);
+              // 2^(top - 127 - 13) in two factors: it may lie outside fp32's normal range
+              const float ml = e8m0_f32(min(254u, max(tl, 1u) - 1u)), mh = e8m0_f32(min(254u, max(th, 1u) - 1u));
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                acc[n][0] = fmaf(d[n][0] * 0x1p-13f, ml, acc[n][0]);
+                acc[n][1] = fmaf(d[n][1] * 0x1p-13f, ml, acc[n][1]);
+                acc[n][2] = fmaf(d[n][2] * 0x1p-13f, mh, acc[n][2]);
+                acc[n][3] = fmaf(d[n][3] * 0x1p-13f, mh, acc[n][3]);
+              }
+              rest = (inl ? 0u : rl) | ((inh ? 0u : rh) << 16);
+            }
           }
         }
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) xp[n] += 128;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    // ---- rows g and g + 8, columns 8 n + 2 c (+ 1): the unit's result, or the warp's share of it
-    if (ja == 0 && jb == S) {
-      const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + t.e) : 1.f;
+      // rows g and g + 8, columns 8 n + 2 c (+ 1): the CTA's result of the unit, or the warp's share
+      const bool whole = ja == 0 && jb == S;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int m = 8 * n + 2 * c + (q & 1), r = t.n0 + g + (q >> 1) * 8;
-          const float y = acc[n][q] * gmul;
-          if (m < t.rows && r < N) a.Y[int64_t(t.row + m) * N + r] = uint16_t(pack_bf16x2(y, y));
+          const int m = 8 * n + 2 * c + (q & 1), r = g + (q >> 1) * 8;
+          const float y = acc[n][q] * rscale[m] * gmul;
+          // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
+          if (!whole) {
+            part[2 * warp + (ja == 0)][r][m] = y;
+          } else if (a.split > 1) {
+            sums[u][r][m] = y;
+          } else if (m < rows && nb0 + u * 16 + r < N) {
+            a.Y[int64_t(row + m) * N + nb0 + u * 16 + r] = uint16_t(pack_bf16x2(y, y));
+          }
         }
-    } else {
-      // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: a later one ends it
-      float (*p)[8 * NT] = part[2 * warp + (ja == 0)];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) p[g + (q >> 1) * 8][8 * n + 2 * c + (q & 1)] = acc[n][q];
+      at += jb - ja;
+      ++u;
+      ja = 0;
+      if (at < end) {
+        open(u, 0);
+        fill(0, min(S, end - at));
+        load_scales(0);
+      }
     }
-  }
-  __syncthreads();
-  // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
-  const int s0 = first_of(warp), u = s0 / S, ub = u * S;  // the unit of the warp's first step, and that unit's first
-  if (s0 < end && s0 > ub && end >= ub + S) {
-    int v = warp - 1;
-    while (first_of(v) > ub) --v;
-    const Unit t = unit_of(u0 + u);
-    const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + t.e) : 1.f;
-    for (int i = lane; i < 16 * 8 * NT; i += 32) {
-      const int r = i & 15, m = i >> 4;
-      float y = 0.f;
-      for (int w = v; w <= warp; ++w)
-        if (first_of(w) < first_of(w + 1)) y += part[2 * w + (first_of(w) <= ub)][r][m];
-      y *= gmul;
-      if (m < t.rows && t.n0 + r < N) a.Y[int64_t(t.row + m) * N + t.n0 + r] = uint16_t(pack_bf16x2(y, y));
+    __syncthreads();
+    // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
+    const int s0 = first_of(warp), us = s0 / S, ub = us * S;  // the unit of the warp's first step, and that unit's first
+    if (s0 < end && s0 > ub && end >= ub + S) {
+      int v = warp - 1;
+      while (first_of(v) > ub) --v;
+      for (int i = lane; i < 16 * 8 * NT; i += 32) {
+        const int r = i & 15, m = i >> 4;
+        float y = 0.f;
+        for (int w = v; w <= warp; ++w)
+          if (first_of(w) < first_of(w + 1)) y += part[2 * w + (first_of(w) <= ub)][r][m];
+        if (a.split > 1) {
+          sums[us][r][m] = y;
+        } else if (m < rows && nb0 + us * 16 + r < N) {
+          a.Y[int64_t(row + m) * N + nb0 + us * 16 + r] = uint16_t(pack_bf16x2(y, y));
+        }
+      }
     }
+    if (a.split > 1) {
+      cluster_sync();  // every CTA of the cluster has its sums in shared memory
+      for (int i = rank * int(blockDim.x) + threadIdx.x; i < (u1 - u0) * 128 * NT; i += a.split * int(blockDim.x)) {
+        const int r = i & 15, m = (i >> 4) % (8 * NT), uu = i / (128 * NT);
+        if (m >= rows || nb0 + uu * 16 + r >= N) continue;
+        const uint32_t at_sum = smem_u32(&sums[uu][r][m]);
+        float y = 0.f;
+        for (int k = 0; k < a.split; ++k) y += ld_shared_cluster_f32(map_shared_rank(at_sum, uint32_t(k)));
+        a.Y[int64_t(row + m) * N + nb0 + uu * 16 + r] = uint16_t(pack_bf16x2(y, y));
+      }
+      cluster_sync();  // the sums stay until every rank has read them
+    }
+    u0 = u1;
   }
 }
 

@@ -632,17 +632,47 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
   return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
 }
 
-// The mma.sync form for few rows per expert: one CTA per SM over units of 16 weight rows.
+// The mma.sync form for few rows per expert.  CTAs of a cluster that share K: as many as it
+// takes for a tile's rows to fit shared memory (0: more than a portable cluster).
+template <int NT>
+int expert_gemv_split(int64_t K) {
+  const int64_t steps = (K + 127) / 128;
+  for (int sp = 1; sp <= 8; sp *= 2)
+    if ((steps + sp - 1) / sp <= wq::VecShape<NT>::MAX_STEPS) return sp;
+  return 0;
+}
+
 template <int FMT, int G, int NT, bool FULL>
-int launch_expert_gemv_full(const wq::ExpertArgs& a, cudaStream_t st) {
+int launch_expert_gemv_full(wq::ExpertArgs a, cudaStream_t st) {
+  using V = wq::VecShape<NT>;
   const int64_t holders = std::min(a.E, a.T);
   const int64_t units = (holders + a.T / (8 * NT)) * ((int64_t(a.N) + 15) / 16);
   static std::atomic<uint64_t> attr_done{0};
-  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT, FULL>, wq::kVecSmem, &attr_done,
-                               "expert gemv smem attribute"))
+  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT, FULL>, V::OFF_X + V::MAX_STEPS * V::STEP_BYTES,
+                               &attr_done, "expert gemv smem attribute"))
     return e;
-  return launch_pdl(wq::expert_gemv_kernel<FMT, G, NT, FULL>, dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas))),
-                    dim3(wq::kVecWarps * 32), wq::kVecSmem, st, "expert gemv launch", a);
+  a.split = expert_gemv_split<NT>(a.K);
+  const int64_t steps = (a.K + 127) / 128;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas / a.split) * a.split), 1, 1);
+  cfg.blockDim = dim3(wq::kVecWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = size_t(V::OFF_X + (steps + a.split - 1) / a.split * V::STEP_BYTES);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  if (a.split > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = a.split;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemv_kernel<FMT, G, NT, FULL>, a), "expert gemv launch");
 }
 
 template <int FMT, int G, int NT>
@@ -651,20 +681,28 @@ int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
                         : launch_expert_gemv_full<FMT, G, NT, false>(a, st);
 }
 
+// Tiles of 8 rows of X, or of 16 where an expert has more (5 on average already leaves
+// many above 8); false: not served.
+bool expert_gemv_serves(const wq::ExpertArgs& a, bool* wide) {
+  const int64_t holders = std::min(a.E, a.T);
+  if (a.T > 16 * holders) return false;
+  *wide = a.E == 1 ? a.T > 8 : a.T > 5 * holders;
+  return (*wide ? expert_gemv_split<2>(a.K) : expert_gemv_split<1>(a.K)) > 0;
+}
+
 template <int FMT, int G>
-int launch_expert_gemv_g(const wq::ExpertArgs& a, cudaStream_t st) {
-  return a.T <= 5 * std::min(a.E, a.T) || (a.E == 1 && a.T <= 8) ? launch_expert_gemv_nt<FMT, G, 1>(a, st)
-                                                                 : launch_expert_gemv_nt<FMT, G, 2>(a, st);
+int launch_expert_gemv_g(const wq::ExpertArgs& a, bool wide, cudaStream_t st) {
+  return wide ? launch_expert_gemv_nt<FMT, G, 2>(a, st) : launch_expert_gemv_nt<FMT, G, 1>(a, st);
 }
 
 template <int FMT>
-int launch_expert_gemv(const wq::ExpertArgs& a, cudaStream_t st) {
+int launch_expert_gemv(const wq::ExpertArgs& a, bool wide, cudaStream_t st) {
   if constexpr (FMT == wq::GEMM_INT4)
-    return a.log2g == 5   ? launch_expert_gemv_g<FMT, 32>(a, st)
-           : a.log2g == 6 ? launch_expert_gemv_g<FMT, 64>(a, st)
-                          : launch_expert_gemv_g<FMT, 128>(a, st);
+    return a.log2g == 5   ? launch_expert_gemv_g<FMT, 32>(a, wide, st)
+           : a.log2g == 6 ? launch_expert_gemv_g<FMT, 64>(a, wide, st)
+                          : launch_expert_gemv_g<FMT, 128>(a, wide, st);
   else
-    return launch_expert_gemv_g<FMT, 0>(a, st);
+    return launch_expert_gemv_g<FMT, 0>(a, wide, st);
 }
 
 template <int FMT>
@@ -674,10 +712,11 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   const int64_t holders = std::min(a.E, a.T);
   const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
   if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(192), st);
-  if (a.T / holders <= 16) {
+  bool wide = false;
+  if (expert_gemv_serves(a, &wide)) {
     wq::ExpertArgs v = a;
     v.X = X; v.packed = static_cast<const uint8_t*>(packed);
-    return launch_expert_gemv<FMT>(v, st);
+    return launch_expert_gemv<FMT>(v, wide, st);
   }
   const int64_t n = items(64);
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
