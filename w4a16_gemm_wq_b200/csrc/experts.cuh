@@ -1179,4 +1179,202 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   }
 }
 
+// ---------------------------------------------------------------------------
+// One or two rows of X per product: multiply-adds on the CUDA cores, which take fewer
+// instructions a weight here (1.5 to 2, and one more for a second row) than the MMA form
+// above (about 2.5), need no staging and no barrier before the weights are under way.
+//
+// A warp takes 8 weight rows over every `ksplit`-th 1024 k (lane: 32 consecutive k, one
+// 16-byte load a row), all rows' loads in flight at once; the grid's y is the row of X,
+// whose expert every warp finds by itself from all the offsets.  A lane scales its own 32
+// activations by a power of two that puts their largest finite magnitude at 2^14, so
+// that fp16 holds them (exactly, down to 2^-31 of that magnitude), and undoes it in its
+// fp32 sum.  INT4: 16 sum (1 + q / 16) x - (16 + z) sum x; E2M1: the converted code times
+// x, the block scales on the sums.
+constexpr int kRowWarps = 8;
+constexpr int kRowRows = 8;
+
+template <int FMT, int MT>
+__global__ void __launch_bounds__(kRowWarps * 32) expert_row_kernel(const __grid_constant__ ExpertArgs a, int ksplit) {
+  __shared__ float part[kRowWarps][kRowRows * MT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % ksplit, rb = blockIdx.x * (kRowWarps / ksplit) + warp / ksplit;
+  const int n0 = rb * kRowRows, i0 = blockIdx.y;  // first weight row, first row of X
+  const int K = a.K, N = a.N;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int e = 0;
+  if (a.offsets) {
+    int found = -1;
+    bool bad = false;
+    for (int b = lane; b < a.E; b += 32) {
+      const int lo = __ldg(a.offsets + b), hi = __ldg(a.offsets + b + 1);
+      bad |= lo < 0 || hi < lo || hi > a.T;
+      if (lo <= i0 && i0 < hi) found = b;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (blockIdx.x == 0 && i0 == 0 && threadIdx.x == 0) report_error(ERR_OFFSETS);
+      return;  // the same for every warp of the grid
+    }
+    e = __reduce_max_sync(0xffffffffu, found);
+    if (e < 0) return;  // a row of no expert
+  }
+  const int64_t row0 = int64_t(e) * N + n0;
+  const int rows = min(kRowRows, N - n0);  // none for the last CTA's spare warps
+  float acc[kRowRows][MT];
+#pragma unroll
+  for (int r = 0; r < kRowRows; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
+
+  if (rows > 0) {
+#pragma unroll 1
+    for (int k0 = sub * 1024; k0 < K; k0 += ksplit * 1024) {
+      const int k = k0 + lane * 32;
+      if (k >= K) break;  // K % 32 == 0: a lane's 32 k are all in or all out
+      uint4 w[kRowRows];
+#pragma unroll
+      for (int r = 0; r < kRowRows; ++r)
+        w[r] = tc_ld_stream(a.packed + (row0 + min(r, rows - 1)) * (K >> 1) + (k >> 1));
+      uint32_t sc[kRowRows], zp[kRowRows];  // raw: nothing waits for them yet
+#pragma unroll
+      for (int r = 0; r < kRowRows; ++r) {
+        const int64_t row = row0 + min(r, rows - 1);
+        zp[r] = 0x88888888u;
+        if (FMT == GEMM_INT4) {
+          const int ng = K >> a.log2g, g = k >> a.log2g;
+          sc[r] = ldg_u16(a.scales + row * ng + g);
+          if (a.zeros) zp[r] = __ldg(a.zeros + row * ((ng + 7) >> 3) + (g >> 3));
+        } else if (FMT == GEMM_NVFP4) {
+          sc[r] = ldg_u16(a.bscale + row * (K >> 4) + (k >> 4));
+        } else {
+          sc[r] = ldg_u8(a.bscale + row * (K >> 5) + (k >> 5));
+        }
+      }
+      // the lane's activations as fp16 pairs (INT4: {x0, x4} {x1, x5} {x2, x6} {x3, x7} of eight)
+      uint32_t xh[MT][16];
+      float back[MT], sum[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float v[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 x = ldg_v4(a.X + int64_t(i0 + m) * K + k + 8 * q);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[8 * q + 2 * j] = __uint_as_float(xw[j] << 16);
+            v[8 * q + 2 * j + 1] = __uint_as_float(xw[j] & 0xFFFF0000u);
+          }
+        }
+        if (FMT == GEMM_MXFP4 && a.inv_s) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(a.inv_s + k) + q);
+            v[4 * q] *= f.x; v[4 * q + 1] *= f.y; v[4 * q + 2] *= f.z; v[4 * q + 3] *= f.w;
+          }
+        }
+        uint32_t top = 0;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+          top = max(top, b < 0x7F800000u ? b : 0u);
+          s += v[j];
+        }
+        const uint32_t fe = min(254u, 268u - max(top >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
+        const float up = __uint_as_float(fe << 23);
+        back[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
+        sum[m] = s;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            xh[m][4 * q + j] = FMT == GEMM_INT4 ? pack_f16x2(v[8 * q + j] * up, v[8 * q + j + 4] * up)
+                                                : pack_f16x2(v[8 * q + 2 * j] * up, v[8 * q + 2 * j + 1] * up);
+      }
+#pragma unroll
+      for (int r = 0; r < kRowRows; ++r) {
+        const uint32_t ww[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+        float d[MT][2];  // E2M1: the lane's two blocks of 16; INT4: two chains
+#pragma unroll
+        for (int m = 0; m < MT; ++m) d[m][0] = d[m][1] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[4];
+          if (FMT == GEMM_INT4) {
+            constexpr uint32_t M = 0x03C003C0u, B = 0x3C003C00u;  // fp16 1 + q / 16: the code at bits 6-9
+            p[0] = lop3_andor(ww[q] << 6, M, B);
+            p[1] = lop3_andor(ww[q] << 2, M, B);
+            p[2] = lop3_andor(ww[q] >> 2, M, B);
+            p[3] = lop3_andor(ww[q] >> 6, M, B);
+          } else {
+            p[0] = e2m1x2_of_byte<0>(ww[q]);
+            p[1] = e2m1x2_of_byte<1>(ww[q]);
+            p[2] = e2m1x2_of_byte<2>(ww[q]);
+            p[3] = e2m1x2_of_byte<3>(ww[q]);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            float& s = d[m][q >> 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s = fma_f16_f32<0, 0>(p[j], xh[m][4 * q + j], s);
+              s = fma_f16_f32<1, 1>(p[j], xh[m][4 * q + j], s);
+            }
+          }
+        }
+        float f0, f1, z = 0.f;
+        if (FMT == GEMM_INT4) {
+          f0 = f1 = __half2float(__ushort_as_half(uint16_t(sc[r])));
+          z = 16.f + float((zp[r] >> (4 * ((k >> a.log2g) & 7))) & 15u);
+        } else if (FMT == GEMM_NVFP4) {
+          const uint32_t h = tc_e4m3x2(sc[r] & 0x7F7Fu);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          f0 = f.x;
+          f1 = f.y;
+        } else {
+          f0 = f1 = e8m0_f32(sc[r]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (FMT == GEMM_INT4)
+            acc[r][m] += f0 * (16.f * ((d[m][0] + d[m][1]) * back[m]) - z * sum[m]);
+          else
+            acc[r][m] += (f0 * (d[m][0] * back[m])) + (f1 * (d[m][1] * back[m]));
+        }
+      }
+    }
+  }
+  // ---- sums over the lanes: eight rows at once, half of them handed over at each of three exchanges
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    float v[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = acc[r][m];
+#pragma unroll
+    for (int h = 4; h >= 1; h >>= 1) {
+      const bool up = (lane & (h * 4)) != 0;
+#pragma unroll
+      for (int r = 0; r < h; ++r) {
+        const float give = up ? v[r] : v[r + h], keep = up ? v[r + h] : v[r];
+        v[r] = keep + __shfl_xor_sync(0xffffffffu, give, h * 4);
+      }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    if ((lane & 3) == 0) part[warp][(lane >> 2) * MT + m] = v[0];  // row lane / 4
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < kRowWarps / ksplit * kRowRows * MT) {
+    const int b = t / (kRowRows * MT), r = t / MT % kRowRows, m = t % MT;
+    const int n = (blockIdx.x * (kRowWarps / ksplit) + b) * kRowRows + r;
+    float y = 0.f;
+    for (int w = 0; w < ksplit; ++w) y += part[b * ksplit + w][r * MT + m];
+    if (FMT == GEMM_NVFP4) y *= __ldg(a.gscale + e);
+    if (n < N) a.Y[int64_t(i0 + m) * N + n] = uint16_t(pack_bf16x2(y, y));
+  }
+}
+
 }  // namespace wq

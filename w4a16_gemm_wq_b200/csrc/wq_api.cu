@@ -705,6 +705,23 @@ int launch_expert_gemv(const wq::ExpertArgs& a, bool wide, cudaStream_t st) {
     return launch_expert_gemv_g<FMT, 0>(a, wide, st);
 }
 
+// The CUDA-core form, one row of X at a time (MT = 2: the two rows of a plain product).
+constexpr int kExpertRowsMax = 16;
+template <int FMT, int MT>
+int launch_expert_rows_mt(const wq::ExpertArgs& a, cudaStream_t st) {
+  // warps that share a row block along K: as many as it has runs of 1024 k, a power of two
+  int ksplit = 1;
+  while (ksplit < wq::kRowWarps && ksplit * 2 <= (a.K + 1023) / 1024) ksplit *= 2;
+  const int per = wq::kRowRows * wq::kRowWarps / ksplit;
+  return launch_pdl(wq::expert_row_kernel<FMT, MT>, dim3(unsigned((a.N + per - 1) / per), unsigned(a.T / MT)),
+                    dim3(wq::kRowWarps * 32), 0, st, "expert row launch", a, ksplit);
+}
+
+template <int FMT>
+int launch_expert_rows(const wq::ExpertArgs& a, cudaStream_t st) {
+  return !a.offsets && a.T == 2 ? launch_expert_rows_mt<FMT, 2>(a, st) : launch_expert_rows_mt<FMT, 1>(a, st);
+}
+
 template <int FMT>
 int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* packed, cudaStream_t st) {
   // the host does not know how the rows fall on the experts: at most min(E, T) hold any, and
@@ -712,12 +729,13 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   const int64_t holders = std::min(a.E, a.T);
   const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
   if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(192), st);
+  wq::ExpertArgs v = a;
+  v.X = X; v.packed = static_cast<const uint8_t*>(packed);
+  // rows of X one by one (both rows of a plain product): few enough that no expert is likely
+  // to hold several
+  if (a.offsets ? a.T <= kExpertRowsMax : a.T <= 2) return launch_expert_rows<FMT>(v, st);
   bool wide = false;
-  if (expert_gemv_serves(a, &wide)) {
-    wq::ExpertArgs v = a;
-    v.X = X; v.packed = static_cast<const uint8_t*>(packed);
-    return launch_expert_gemv<FMT>(v, wide, st);
-  }
+  if (expert_gemv_serves(a, &wide)) return launch_expert_gemv<FMT>(v, wide, st);
   const int64_t n = items(64);
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
   const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
