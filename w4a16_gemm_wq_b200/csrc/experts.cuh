@@ -1184,8 +1184,9 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 // instructions a weight here (1.5 to 2, and one more for a second row) than the MMA form
 // above (about 2.5), need no staging and no barrier before the weights are under way.
 //
-// A warp takes 8 weight rows over every `ksplit`-th 1024 k (lane: 32 consecutive k, one
-// 16-byte load a row), all rows' loads in flight at once; the grid's y is the row of X,
+// A warp takes 8 weight rows over every `ksplit`-th 1024 k (lane: 32 consecutive k, 16
+// bytes a row), all rows' codes by cp.async into slots that the lane reads itself, which
+// leaves few enough registers for three CTAs on an SM; the grid's y is the row of X,
 // whose expert every warp finds by itself from all the offsets.  A lane scales its own 32
 // activations by a power of two that puts their largest finite magnitude at 2^14, so
 // that fp16 holds them (exactly, down to 2^-31 of that magnitude), and undoes it in its
@@ -1195,8 +1196,10 @@ constexpr int kRowWarps = 8;
 constexpr int kRowRows = 8;
 
 template <int FMT, int MT>
-__global__ void __launch_bounds__(kRowWarps * 32) expert_row_kernel(const __grid_constant__ ExpertArgs a, int ksplit) {
+__global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
+    expert_row_kernel(const __grid_constant__ ExpertArgs a, int ksplit) {
   __shared__ float part[kRowWarps][kRowRows * MT];
+  extern __shared__ __align__(16) uint8_t row_smem[];  // codes: [2][warp][row][32 lanes][16 bytes]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % ksplit, rb = blockIdx.x * (kRowWarps / ksplit) + warp / ksplit;
   const int n0 = rb * kRowRows, i0 = blockIdx.y;  // first weight row, first row of X
@@ -1228,74 +1231,103 @@ __global__ void __launch_bounds__(kRowWarps * 32) expert_row_kernel(const __grid
     for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
 
   if (rows > 0) {
-#pragma unroll 1
-    for (int k0 = sub * 1024; k0 < K; k0 += ksplit * 1024) {
-      const int k = k0 + lane * 32;
-      if (k >= K) break;  // K % 32 == 0: a lane's 32 k are all in or all out
-      uint4 w[kRowRows];
+    const uint32_t slots = smem_u32(row_smem) + uint32_t(warp * kRowRows * 512 + lane * 16);
+    const uint8_t* codes = a.packed + row0 * (K >> 1) + lane * 16;
+    const int last = rows - 1;
+    const auto request = [&](int k0, uint32_t dst) {  // a lane's 32 k are all in or all out: K % 32 == 0
+      const bool in = k0 + lane * 32 < K;
+      const uint8_t* p = codes + (k0 >> 1);
 #pragma unroll
       for (int r = 0; r < kRowRows; ++r)
-        w[r] = tc_ld_stream(a.packed + (row0 + min(r, rows - 1)) * (K >> 1) + (k >> 1));
-      uint32_t sc[kRowRows], zp[kRowRows];  // raw: nothing waits for them yet
+        cp_async_zfill<16>(dst + r * 512, in ? p + min(r, last) * int64_t(K >> 1) : a.packed, in ? 16 : 0);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint32_t slot = slots;
+    request(sub * 1024, slot);
+#pragma unroll 1
+    for (int k0 = sub * 1024; k0 < K; k0 += ksplit * 1024) {
+      const uint32_t here = slot;
+      slot = slot == slots ? slots + kRowWarps * kRowRows * 512 : slots;
+      if (k0 + ksplit * 1024 < K) {
+        request(k0 + ksplit * 1024, slot);
+      } else {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      const int k = k0 + lane * 32;
+      if (k >= K) break;
+      // raw scales and zero-point words: nothing waits for them yet
+      uint32_t sc[kRowRows], zp[kRowRows];
+      {
+        const int ng = K >> a.log2g, g = k >> a.log2g;
+        const int sw = FMT == GEMM_INT4 ? 2 * ng : FMT == GEMM_NVFP4 ? K >> 4 : K >> 5;
+        const uint8_t* sp = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
+        sp += row0 * sw + (FMT == GEMM_INT4 ? 2 * g : FMT == GEMM_NVFP4 ? k >> 4 : k >> 5);
+        const uint32_t* zq = a.zeros + row0 * ((ng + 7) >> 3) + (g >> 3);
 #pragma unroll
-      for (int r = 0; r < kRowRows; ++r) {
-        const int64_t row = row0 + min(r, rows - 1);
-        zp[r] = 0x88888888u;
-        if (FMT == GEMM_INT4) {
-          const int ng = K >> a.log2g, g = k >> a.log2g;
-          sc[r] = ldg_u16(a.scales + row * ng + g);
-          if (a.zeros) zp[r] = __ldg(a.zeros + row * ((ng + 7) >> 3) + (g >> 3));
-        } else if (FMT == GEMM_NVFP4) {
-          sc[r] = ldg_u16(a.bscale + row * (K >> 4) + (k >> 4));
-        } else {
-          sc[r] = ldg_u8(a.bscale + row * (K >> 5) + (k >> 5));
+        for (int r = 0; r < kRowRows; ++r) {
+          const int64_t rr = min(r, last);
+          sc[r] = FMT == GEMM_MXFP4 ? ldg_u8(sp + rr * sw) : ldg_u16(sp + rr * sw);
+          zp[r] = FMT == GEMM_INT4 && a.zeros ? __ldg(zq + rr * ((ng + 7) >> 3)) : 0x88888888u;
         }
       }
-      // the lane's activations as fp16 pairs (INT4: {x0, x4} {x1, x5} {x2, x6} {x3, x7} of eight)
+      // the lane's activations (times 1/s) as fp16 pairs (INT4: {x0, x4} {x1, x5} {x2, x6} {x3, x7}
+      // of eight), written over the bf16 ones
       uint32_t xh[MT][16];
       float back[MT], sum[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        float v[32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint4 x = ldg_v4(a.X + int64_t(i0 + m) * K + k + 8 * q);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[8 * q + 2 * j] = __uint_as_float(xw[j] << 16);
-            v[8 * q + 2 * j + 1] = __uint_as_float(xw[j] & 0xFFFF0000u);
-          }
+          xh[m][4 * q] = x.x; xh[m][4 * q + 1] = x.y; xh[m][4 * q + 2] = x.z; xh[m][4 * q + 3] = x.w;
         }
-        if (FMT == GEMM_MXFP4 && a.inv_s) {
+      }
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(a.inv_s + k) + q);
-            v[4 * q] *= f.x; v[4 * q + 1] *= f.y; v[4 * q + 2] *= f.z; v[4 * q + 3] *= f.w;
+      for (int m = 0; m < MT; ++m) {
+        const bool scaled = FMT == GEMM_MXFP4 && a.inv_s;
+        const auto pair = [&](int j) {  // elements 2j and 2j + 1
+          float2 f = make_float2(__uint_as_float(xh[m][j] << 16), __uint_as_float(xh[m][j] & 0xFFFF0000u));
+          if (scaled) {
+            const float2 i = __ldg(reinterpret_cast<const float2*>(a.inv_s + k + 2 * j));
+            f.x *= i.x;
+            f.y *= i.y;
           }
-        }
+          return f;
+        };
         uint32_t top = 0;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-          top = max(top, b < 0x7F800000u ? b : 0u);
-          s += v[j];
+        for (int j = 0; j < 16; ++j) {
+          const float2 f = pair(j);
+          const uint32_t b0 = __float_as_uint(f.x) & 0x7FFFFFFFu, b1 = __float_as_uint(f.y) & 0x7FFFFFFFu;
+          top = max(top, max(b0 < 0x7F800000u ? b0 : 0u, b1 < 0x7F800000u ? b1 : 0u));
+          if (FMT == GEMM_INT4) s += f.x + f.y;
         }
         const uint32_t fe = min(254u, 268u - max(top >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
         const float up = __uint_as_float(fe << 23);
         back[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
         sum[m] = s;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            xh[m][4 * q + j] = FMT == GEMM_INT4 ? pack_f16x2(v[8 * q + j] * up, v[8 * q + j + 4] * up)
-                                                : pack_f16x2(v[8 * q + 2 * j] * up, v[8 * q + 2 * j + 1] * up);
+        for (int q = 0; q < 4; ++q) {
+          const float2 f0 = pair(4 * q), f1 = pair(4 * q + 1), f2 = pair(4 * q + 2), f3 = pair(4 * q + 3);
+          if (FMT == GEMM_INT4) {
+            xh[m][4 * q] = pack_f16x2(f0.x * up, f2.x * up);
+            xh[m][4 * q + 1] = pack_f16x2(f0.y * up, f2.y * up);
+            xh[m][4 * q + 2] = pack_f16x2(f1.x * up, f3.x * up);
+            xh[m][4 * q + 3] = pack_f16x2(f1.y * up, f3.y * up);
+          } else {
+            xh[m][4 * q] = pack_f16x2(f0.x * up, f0.y * up);
+            xh[m][4 * q + 1] = pack_f16x2(f1.x * up, f1.y * up);
+            xh[m][4 * q + 2] = pack_f16x2(f2.x * up, f2.y * up);
+            xh[m][4 * q + 3] = pack_f16x2(f3.x * up, f3.y * up);
+          }
+        }
       }
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
       for (int r = 0; r < kRowRows; ++r) {
-        const uint32_t ww[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+        const uint4 w = ld_shared_v4(here + r * 512);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
         float d[MT][2];  // E2M1: the lane's two blocks of 16; INT4: two chains
 #pragma unroll
         for (int m = 0; m < MT; ++m) d[m][0] = d[m][1] = 0.f;
@@ -1346,6 +1378,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) expert_row_kernel(const __grid
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   // ---- sums over the lanes: eight rows at once, half of them handed over at each of three exchanges
 #pragma unroll
   for (int m = 0; m < MT; ++m) {

@@ -713,8 +713,11 @@ int launch_expert_rows_mt(const wq::ExpertArgs& a, cudaStream_t st) {
   int ksplit = 1;
   while (ksplit < wq::kRowWarps && ksplit * 2 <= (a.K + 1023) / 1024) ksplit *= 2;
   const int per = wq::kRowRows * wq::kRowWarps / ksplit;
+  constexpr int kSmem = 2 * wq::kRowWarps * wq::kRowRows * 512;
+  static std::atomic<uint64_t> attr_done{0};
+  if (int e = ensure_smem_attr(wq::expert_row_kernel<FMT, MT>, kSmem, &attr_done, "expert row smem attribute")) return e;
   return launch_pdl(wq::expert_row_kernel<FMT, MT>, dim3(unsigned((a.N + per - 1) / per), unsigned(a.T / MT)),
-                    dim3(wq::kRowWarps * 32), 0, st, "expert row launch", a, ksplit);
+                    dim3(wq::kRowWarps * 32), kSmem, st, "expert row launch", a, ksplit);
 }
 
 template <int FMT>
