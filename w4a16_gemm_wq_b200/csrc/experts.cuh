@@ -756,32 +756,36 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 // X is staged once per row tile in the order of the MMA's B fragments, each row scaled
 // by a power of two that puts its largest finite magnitude at 2^14: fp16 then holds
 // bf16 exactly down to 2^-31 of that magnitude, and what is smaller to 2^-39 of it.
-// Codes come by cp.async, kVecDepth - 1 steps ahead, into slots that the copying lane
-// reads itself (no barrier, and a loop body of one step: a body unrolled over the steps
-// in flight spent the short kernel's time on instruction fetches); scales one step
-// ahead into registers.
+// Two steps at a time: one alone left the warp waiting for its own results.  Codes come
+// by cp.async, four to six steps ahead and on into the warp's next unit, into slots that
+// the copying lane reads itself (no barrier, and a loop body of two steps: one unrolled
+// over all that is in flight spent the short kernel's time on instruction fetches); scales
+// two steps ahead into registers.
 // Lane (g, c) (g = lane / 4, c = lane % 4) holds codes of rows g and g + 8; the k order
 // inside an MMA is free, so its four k of each are four of the lane's own:
 //   INT4   lane c takes G / 4 k of every group, so that an MMA stays inside a group: A is
-//          q - z or 16 (q - z) (exact; X of the latter staged / 16), and the fp16 scale
-//          multiplies the group's fp32 sums;
+//          1024 + q or 1024 + 16 q (one logic instruction a pair; X of the latter staged
+//          / 16), and the group's fp32 sums lose what the 1024 and the zero point z added,
+//          P + z Q from sums of the staged X, before the fp16 scale multiplies them (the
+//          cancellation costs eight of fp32's bits, 2^-16 of the sum of magnitudes);
 //   NVFP4  lane c takes 32 k in a row; A is the code times its block scale (exact);
 //   MXFP4  the same, with the block scale relative to the largest of the row's step, and
 //          the step's fp32 sums times that one; blocks under 2^-26 of it take another turn.
 constexpr int kVecWarps = 16;
-constexpr int kVecDepth = 4;
+constexpr int kVecDepth = 6;
 constexpr int kVecRing = kVecWarps * kVecDepth * 1024;
 
 // Shared memory: codes [warp][kVecDepth][2][32 lanes][16 bytes], the CTA's sums of a run of units
 // (where a cluster shares them), sums of units that straddle warps, X fragments.
-template <int NT>
+template <int FMT, int NT>
 struct VecShape {
   static constexpr int SUM_BYTES = 16 * 8 * NT * 4;              // one unit's sums
-  static constexpr int MAX_UNITS = 16;
+  static constexpr int MAX_UNITS = 16 / NT;
   static constexpr int OFF_SUMS = kVecRing;
   static constexpr int OFF_PART = OFF_SUMS + MAX_UNITS * SUM_BYTES;
   static constexpr int OFF_X = OFF_PART + 2 * kVecWarps * SUM_BYTES;
-  static constexpr int STEP_BYTES = NT * 2048;                   // X fragments of a step
+  static constexpr int FRAG_BYTES = NT * 2048;                   // X fragments of a step
+  static constexpr int STEP_BYTES = FRAG_BYTES + (FMT == GEMM_INT4 ? NT * 256 : 0);  // and P, Q of its groups
   static constexpr int MAX_STEPS = (216 * 1024 - OFF_X) / STEP_BYTES;
 };
 
@@ -792,17 +796,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // FULL: K % 128 == 0, no step reaches past K (and a step's scales of a row are aligned words).
 template <int FMT, int G, int NT, bool FULL>
 __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __grid_constant__ ExpertArgs a) {
   static_assert(FMT != GEMM_INT4 || G == 32 || G == 64 || G == 128, "group size");
-  using V = VecShape<NT>;
+  using V = VecShape<FMT, NT>;
   constexpr int NG = FMT == GEMM_INT4 ? 128 / G : 1;    // groups of a step
   constexpr int WPG = 4 / NG;                           // words (8 k) of a lane per group
   extern __shared__ __align__(1024) uint8_t vec_smem[];
@@ -864,25 +862,28 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     int at = first_of(warp);
     const int end = first_of(warp + 1);
 
-    // ---- cursors of a unit's steps: codes kVecDepth - 1 steps ahead, scales one step ahead
+    // ---- cursors over the run's steps, on into the next unit: codes and scales
+    const auto row_of = [&](int u, int r) { return int64_t(e) * N + min(nb0 + u * 16 + r, N - 1); };
     const uint8_t *plo, *phi, *slo, *shi, *zlo, *zhi;
-    uint32_t put, take;
-    const auto open = [&](int u, int j) {  // at step j of unit u
-      const int64_t rlo = int64_t(e) * N + min(nb0 + u * 16 + g, N - 1);
-      const int64_t d = int64_t(e) * N + min(nb0 + u * 16 + g + 8, N - 1) - rlo;
-      plo = a.packed + rlo * (K >> 1) + (S0 + j) * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
-      phi = plo + d * (K >> 1);
-      slo = scales + rlo * sw + (S0 + j) * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
+    int cu = 0, cj = 0, su = 0, sj = 0;  // unit and step of the next request and of the next scales
+    uint32_t put = ring;
+    const auto open_codes = [&]() {
+      const int64_t rlo = row_of(cu, g), rhi = row_of(cu, g + 8);
+      plo = a.packed + rlo * (K >> 1) + (S0 + cj) * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
+      phi = plo + (rhi - rlo) * (K >> 1);
+    };
+    const auto open_scales = [&]() {
+      const int64_t rlo = row_of(su, g), d = row_of(su, g + 8) - rlo;
+      slo = scales + rlo * sw + (S0 + sj) * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
       shi = slo + d * sw;
       zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
       zhi = zlo + d * zw;
-      put = take = ring;
     };
     // a lane's 16 code bytes of each row, in word order; zeros past K
-    const auto request = [&](int j) {
+    const auto request = [&]() {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const int k0 = (S0 + j) * 128;
+        const int k0 = (S0 + cj) * 128;
         const bool in = FULL || (FMT == GEMM_INT4 ? k0 + i * G < K : k0 + 32 * c < K);
         cp_async_zfill<16 / NG>(put + i * (16 / NG), in ? plo + i * (G / 2) : a.packed, in ? 16 / NG : 0);
         cp_async_zfill<16 / NG>(put + 512 + i * (16 / NG), in ? phi + i * (G / 2) : a.packed, in ? 16 / NG : 0);
@@ -890,102 +891,133 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       plo += 64;
       phi += 64;
       put = put + 1024u == ring + kVecDepth * 1024u ? ring : put + 1024u;
-    };
-    const auto fill = [&](int j0, int j1) {
-#pragma unroll 1
-      for (int i = 0; i < kVecDepth - 1; ++i) {
-        if (j0 + i < j1) request(j0 + i);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+      if (++cj == S) {
+        cj = 0;
+        ++cu;
+        open_codes();
       }
     };
     // scales of rows g and g + 8 (fp16 per group, two E4M3 bytes, or an E8M0 byte) and the bytes
     // that hold the step's zero points (one for G >= 64, else two), as they are loaded: nothing
     // waits for them before the step that uses them
-    uint32_t scl[NG], sch[NG], zpl = 0x8888u, zph = 0x8888u;
-    const auto load_scales = [&](int j) {
+    struct Scales {
+      uint32_t l[NG], h[NG], zl, zh;
+    };
+    const auto load_scales = [&](Scales& r) {
       if (FMT == GEMM_INT4 && FULL && NG > 1) {  // a row's scales of the step as words
 #pragma unroll
         for (int i = 0; i < NG; i += 2) {
-          scl[i] = __ldg(reinterpret_cast<const uint32_t*>(slo + 2 * i));
-          sch[i] = __ldg(reinterpret_cast<const uint32_t*>(shi + 2 * i));
+          r.l[i] = __ldg(reinterpret_cast<const uint32_t*>(slo + 2 * i));
+          r.h[i] = __ldg(reinterpret_cast<const uint32_t*>(shi + 2 * i));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          const bool in = FULL || (FMT == GEMM_INT4 ? ((S0 + j) * NG + i) * 2 < sw : (S0 + j) * 128 + 32 * c < K);
-          scl[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) : ldg_u16(slo + 2 * i);
-          sch[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(shi) : ldg_u16(shi + 2 * i);
+          const bool in = FULL || (FMT == GEMM_INT4 ? ((S0 + sj) * NG + i) * 2 < sw : (S0 + sj) * 128 + 32 * c < K);
+          r.l[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) : ldg_u16(slo + 2 * i);
+          r.h[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(shi) : ldg_u16(shi + 2 * i);
         }
       }
       slo += SB;
       shi += SB;
+      r.zl = r.zh = 0x8888u;
       if (FMT == GEMM_INT4 && a.zeros) {
-        const int b = ((S0 + j) * NG) >> 1;
-        zpl = G == 32 ? ldg_u16(zlo + b) : ldg_u8(zlo + b);
-        zph = G == 32 ? ldg_u16(zhi + b) : ldg_u8(zhi + b);
+        const int b = ((S0 + sj) * NG) >> 1;
+        r.zl = G == 32 ? ldg_u16(zlo + b) : ldg_u8(zlo + b);
+        r.zh = G == 32 ? ldg_u16(zhi + b) : ldg_u8(zhi + b);
+      }
+      if (++sj == S) {
+        sj = 0;
+        ++su;
+        open_scales();
       }
     };
+    Scales r0 = {}, r1 = {};
 
-    int u = 0, ja = 0;
-    if (at < end) {  // the first codes are under way while X is staged
+    int u = 0, j = 0;  // unit and step in hand
+    int todo = end;    // steps whose codes are still to be requested start here
+    if (at < end) {    // the first codes are under way while X is staged
       u = at / S;
-      ja = at - u * S;
-      open(u, ja);
-      fill(ja, min(S, ja + end - at));
-      load_scales(ja);
+      j = at - u * S;
+      cu = su = u;
+      cj = sj = j;
+      open_codes();
+      open_scales();
+      todo = min(end, at + kVecDepth);
+#pragma unroll 1
+      for (int i = 0; i < kVecDepth; ++i) {
+        if (at + i < end) request();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      load_scales(r0);
+      if (at + 1 < end) load_scales(r1);
     }
     if (staged != tile) {
       // X, or X * act_inv_s, 256 k of a row at a time: the rows' largest finite magnitudes, then the fragments
       if (threadIdx.x < 8 * NT) rtop[threadIdx.x] = 0;
       __syncthreads();  // also: the last run's readers are done
       const float* f = FMT == GEMM_MXFP4 && a.inv_s ? a.inv_s + S0 * 128 : nullptr;
-      const int len = min(S * 128, K - S0 * 128), pieces = (S + 1) >> 1;
-      const auto load8 = [&](int m, int k, float (&v)[8]) {
-        if (k >= len) {
+      const int len = min(S * 128, K - S0 * 128);
+      // each row by 2 / NT warps, alternate runs of 256 k
+      constexpr int WPR = kVecWarps / (8 * NT);
+      const int m = warp / WPR, kend = m < rows ? S * 128 : 0;
+      const uint16_t* xrow = a.X + int64_t(row + min(m, rows - 1)) * K + S0 * 128;
+      // four runs' loads in flight at once, twice over (the second time from L1)
+      const auto pass = [&](auto&& use) {
+#pragma unroll 1
+        for (int kk = warp % WPR * 256 + lane * 8; kk - lane * 8 < kend; kk += 4 * WPR * 256) {
+          uint4 r[4];
+          float4 f0[4], f1[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = 0.f;
-          return;
-        }
-        const uint4 r = ldg_v4(a.X + int64_t(row + m) * K + S0 * 128 + k);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+          for (int q = 0; q < 4; ++q) {
+            const int k = kk + q * WPR * 256;
+            r[q] = k < len ? ldg_v4(xrow + k) : make_uint4(0, 0, 0, 0);
+            if (FMT == GEMM_MXFP4) {
+              f0[q] = f1[q] = make_float4(1.f, 1.f, 1.f, 1.f);
+              if (f && k < len) {
+                f0[q] = __ldg(reinterpret_cast<const float4*>(f + k));
+                f1[q] = __ldg(reinterpret_cast<const float4*>(f + k) + 1);
+              }
+            }
+          }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = __uint_as_float(w[j] << 16);
-          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-        if (f) {
-          const float4 f0 = __ldg(reinterpret_cast<const float4*>(f + k)), f1 = __ldg(reinterpret_cast<const float4*>(f + k) + 1);
-          v[0] *= f0.x; v[1] *= f0.y; v[2] *= f0.z; v[3] *= f0.w;
-          v[4] *= f1.x; v[5] *= f1.y; v[6] *= f1.z; v[7] *= f1.w;
+          for (int q = 0; q < 4; ++q) {
+            const int k = kk + q * WPR * 256;
+            const uint32_t w[4] = {r[q].x, r[q].y, r[q].z, r[q].w};
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = __uint_as_float(w[i] << 16);
+              v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+            if (FMT == GEMM_MXFP4) {
+              v[0] *= f0[q].x; v[1] *= f0[q].y; v[2] *= f0[q].z; v[3] *= f0[q].w;
+              v[4] *= f1[q].x; v[5] *= f1[q].y; v[6] *= f1[q].z; v[7] *= f1[q].w;
+            }
+            use(k, v);
+          }
         }
       };
-#pragma unroll 2
-      for (int i = warp; i < rows * pieces; i += kVecWarps) {
-        const int m = i / pieces, k = (i - m * pieces) * 256 + lane * 8;
-        float v[8];
-        load8(m, k, v);
-        uint32_t top = 0;
+      uint32_t top = 0;
+      pass([&](int, float (&v)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
           top = max(top, b < 0x7F800000u ? b : 0u);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) atomicMax(&rtop[m], top);
-      }
+      });
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) atomicMax(&rtop[m], top);
       __syncthreads();
-#pragma unroll 2
-      for (int i = warp; i < rows * pieces; i += kVecWarps) {
-        const int m = i / pieces, k = (i - m * pieces) * 256 + lane * 8;
-        const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
-        const float up = __uint_as_float(fe << 23);
-        if (lane == 0 && k == 0) rscale[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
-        if (k >= S * 128) continue;  // an odd number of steps
-        float v[8];
-        load8(m, k, v);
+      const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
+      const float up = __uint_as_float(fe << 23);
+      if (lane == 0) rscale[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
+      pass([&](int k, float (&v)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= up;
+        for (int i = 0; i < 8; ++i) v[i] *= up;
         const int p = (k & 127) >> 3;  // 8-k piece of the step: word w of lane cc
+        uint8_t* step = vec_smem + V::OFF_X + (k >> 7) * V::STEP_BYTES;
+        const bool in = k < S * 128;   // a run of 256 may pass an odd number of steps
         uint4 o;
         int w, cc;
         if constexpr (FMT == GEMM_INT4) {
@@ -994,172 +1026,212 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           w = (p * 8 / G) * WPG + (p * 8 % (G / 4)) / 8;
           o = make_uint4(pack_f16x2(v[0], v[4]), pack_f16x2(v[1] * 0.0625f, v[5] * 0.0625f), pack_f16x2(v[2], v[6]),
                          pack_f16x2(v[3] * 0.0625f, v[7] * 0.0625f));
+          // what the group's sums hold of 1024 (64 times X where it meets 16 q), and the sum of X
+          const float even = v[0] + v[4] + v[2] + v[6], odd = v[1] + v[5] + v[3] + v[7];
+          float P = 1024.f * even + 64.f * odd, Q = even + odd;
+#pragma unroll
+          for (int h = 1; h < G / 8; h <<= 1) {
+            P += __shfl_xor_sync(0xffffffffu, P, h);
+            Q += __shfl_xor_sync(0xffffffffu, Q, h);
+          }
+          if (in && p * 8 % G == 0)
+            *reinterpret_cast<float2*>(step + V::FRAG_BYTES + ((p * 8 / G) * 8 * NT + m) * 8) = make_float2(P, Q);
         } else {
           cc = p >> 2;
           w = p & 3;
           o = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
         }
-        st_shared_v4(smem_u32(vec_smem) + uint32_t(V::OFF_X + (k >> 7) * V::STEP_BYTES + (m >> 3) * 2048 + w * 512 +
-                                                   (4 * (m & 7) + cc) * 16), o);
-      }
+        if (in) *reinterpret_cast<uint4*>(step + (m >> 3) * 2048 + w * 512 + (4 * (m & 7) + cc) * 16) = o;
+      });
       staged = tile;
       __syncthreads();
     }
 
-    // ---- the warp's steps, unit by unit
-    while (at < end) {
-      const int jb = min(S, ja + end - at);
-      float acc[NT][4];
+    // ---- the warp's steps
+    // one step's products from its codes, scales and fragments
+    const auto products = [&](int j, const uint4& cl4, const uint4& ch4, const Scales& r, float (&acc)[NT][4]) {
+      const uint32_t wl[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, wh[4] = {ch4.x, ch4.y, ch4.z, ch4.w};
+      const uint32_t xs = xfrag + uint32_t(j * V::STEP_BYTES);
+      if (FMT == GEMM_INT4) {
+        const uint32_t pq = smem_u32(vec_smem) + uint32_t(V::OFF_X + V::FRAG_BYTES + j * V::STEP_BYTES + c * 16);
+        float d[NT][4];  // the group's sums
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll 1
-      for (int j = ja; j < jb; ++j) {
-        if (j + kVecDepth - 1 < jb) request(j + kVecDepth - 1);
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group %0;" ::"n"(kVecDepth - 1) : "memory");
-        const uint4 cl4 = ld_shared_v4(take), ch4 = ld_shared_v4(take + 512);
-        take = take + 1024u == ring + kVecDepth * 1024u ? ring : take + 1024u;
-        const uint32_t wl[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, wh[4] = {ch4.x, ch4.y, ch4.z, ch4.w};
-        uint32_t s[NG];  // row g's in the low half
+        for (int w = 0; w < 4; ++w) {
+          constexpr uint32_t B = 0x64006400u;  // fp16 1024: a code under it is 1024 + q (or + 16 q)
+          const uint32_t l8 = wl[w] >> 8, h8 = wh[w] >> 8;
+          const uint32_t a0 = lop3_andor(wl[w], 0x000F000Fu, B), a2 = lop3_andor(wl[w], 0x00F000F0u, B);
+          const uint32_t a1 = lop3_andor(wh[w], 0x000F000Fu, B), a3 = lop3_andor(wh[w], 0x00F000F0u, B);
+          const uint32_t b0 = lop3_andor(l8, 0x000F000Fu, B), b2 = lop3_andor(l8, 0x00F000F0u, B);
+          const uint32_t b1 = lop3_andor(h8, 0x000F000Fu, B), b3 = lop3_andor(h8, 0x00F000F0u, B);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          const bool words = FMT == GEMM_INT4 && FULL && NG > 1;
-          s[i] = prmt_b32(scl[words ? i & ~1 : i], sch[words ? i & ~1 : i], words && (i & 1) ? 0x7632 : 0x5410);
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
+            if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+            mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
+            mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
+          }
+          if (w % WPG == WPG - 1) {
+            const int gi = w / WPG, nib = 4 * ((G == 128 ? ((S0 + j) & 1) : 0) + gi);
+            const bool words = FULL && NG > 1;
+            const uint32_t s2 = prmt_b32(r.l[words ? gi & ~1 : gi], r.h[words ? gi & ~1 : gi],
+                                         words && (gi & 1) ? 0x7632 : 0x5410);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s2));
+            const float zl = __uint_as_float(lop3_andor(r.zl >> nib, 15u, 0x4B000000u)) - 8388608.f;
+            const float zh = __uint_as_float(lop3_andor(r.zh >> nib, 15u, 0x4B000000u)) - 8388608.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 t = ld_shared_v4(pq + uint32_t((gi * NT + n) * 64));  // P, Q of columns 2 c and 2 c + 1
+              const float P0 = __uint_as_float(t.x), Q0 = __uint_as_float(t.y);
+              const float P1 = __uint_as_float(t.z), Q1 = __uint_as_float(t.w);
+              acc[n][0] = fmaf(f.x, fmaf(-zl, Q0, d[n][0] - P0), acc[n][0]);
+              acc[n][1] = fmaf(f.x, fmaf(-zl, Q1, d[n][1] - P1), acc[n][1]);
+              acc[n][2] = fmaf(f.y, fmaf(-zh, Q0, d[n][2] - P0), acc[n][2]);
+              acc[n][3] = fmaf(f.y, fmaf(-zh, Q1, d[n][3] - P1), acc[n][3]);
+            }
+          }
         }
-        const uint32_t z = zpl | (zph << 16);
-        if (j + 1 < jb) load_scales(j + 1);
-        const uint32_t xs = xfrag + uint32_t(j * V::STEP_BYTES);
-        if (FMT == GEMM_INT4) {
-          float d[NT][4];  // the group's sums
+      } else {
+        // A = code times scale; fp16 pairs of the lane's two NVFP4 blocks, or of its MXFP4 block
+        const auto mmas = [&](uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1, float (&d)[NT][4]) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const int nib = 4 * ((G == 128 ? ((S0 + j) & 1) : 0) + w / WPG);  // this group's zero point
-            const uint32_t zl = ((z >> nib) & 15u) * 0x00010001u, zh = ((z >> (16 + nib)) & 15u) * 0x00010001u;
-            constexpr uint32_t B = 0x64006400u;  // fp16 1024: a code under it is 1024 + q (or + 16 q)
-            const uint32_t zl1 = B + zl, zl16 = B + zl * 16u, zh1 = B + zh, zh16 = B + zh * 16u;
-            const uint32_t l8 = wl[w] >> 8, h8 = wh[w] >> 8;
-            const uint32_t a0 = f16x2_sub(lop3_andor(wl[w], 0x000F000Fu, B), zl1);
-            const uint32_t a1 = f16x2_sub(lop3_andor(wh[w], 0x000F000Fu, B), zh1);
-            const uint32_t a2 = f16x2_sub(lop3_andor(wl[w], 0x00F000F0u, B), zl16);
-            const uint32_t a3 = f16x2_sub(lop3_andor(wh[w], 0x00F000F0u, B), zh16);
-            const uint32_t b0 = f16x2_sub(lop3_andor(l8, 0x000F000Fu, B), zl1);
-            const uint32_t b1 = f16x2_sub(lop3_andor(h8, 0x000F000Fu, B), zh1);
-            const uint32_t b2 = f16x2_sub(lop3_andor(l8, 0x00F000F0u, B), zl16);
-            const uint32_t b3 = f16x2_sub(lop3_andor(h8, 0x00F000F0u, B), zh16);
+            const uint32_t sl = w < 2 ? l0 : l1, sh = w < 2 ? h0 : h1;
+            const uint32_t a0 = h2_mul(e2m1x2_of_byte<0>(wl[w]), sl), a2 = h2_mul(e2m1x2_of_byte<1>(wl[w]), sl);
+            const uint32_t b0 = h2_mul(e2m1x2_of_byte<2>(wl[w]), sl), b2 = h2_mul(e2m1x2_of_byte<3>(wl[w]), sl);
+            const uint32_t a1 = h2_mul(e2m1x2_of_byte<0>(wh[w]), sh), a3 = h2_mul(e2m1x2_of_byte<1>(wh[w]), sh);
+            const uint32_t b1 = h2_mul(e2m1x2_of_byte<2>(wh[w]), sh), b3 = h2_mul(e2m1x2_of_byte<3>(wh[w]), sh);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
-              if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
               mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
               mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
-              if (w % WPG == WPG - 1) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s[w / WPG]));
-                acc[n][0] = fmaf(f.x, d[n][0], acc[n][0]);
-                acc[n][1] = fmaf(f.x, d[n][1], acc[n][1]);
-                acc[n][2] = fmaf(f.y, d[n][2], acc[n][2]);
-                acc[n][3] = fmaf(f.y, d[n][3], acc[n][3]);
-              }
             }
           }
+        };
+        if (FMT == GEMM_NVFP4) {
+          const uint32_t fl = tc_e4m3x2(r.l[0] & 0x7F7Fu), fh = tc_e4m3x2(r.h[0] & 0x7F7Fu);
+          mmas(prmt_b32(fl, fl, 0x1010), prmt_b32(fl, fl, 0x3232), prmt_b32(fh, fh, 0x1010),
+               prmt_b32(fh, fh, 0x3232), acc);
         } else {
-          // A = code times scale; fp16 pairs of the lane's two NVFP4 blocks, or of its MXFP4 block
-          const auto products = [&](uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1, float (&d)[NT][4]) {
+          // scale bytes + 1 of the blocks still to be taken, row g's in the low half; a block whose
+          // codes are all zero counts for none (a NaN scale does)
+          const bool zl = ((wl[0] | wl[1] | wl[2] | wl[3]) & 0x77777777u) == 0 && r.l[0] != 255u;
+          const bool zh = ((wh[0] | wh[1] | wh[2] | wh[3]) & 0x77777777u) == 0 && r.h[0] != 255u;
+          uint32_t rest = (zl ? 0u : r.l[0] + 1u) | (zh ? 0u : (r.h[0] + 1u) << 16);
+          const auto turn = [&]() {
+            // the rows' largest scales among them, and the blocks within 2^-26 of those
+            uint32_t top = max_u16x2(rest, __shfl_xor_sync(0xffffffffu, rest, 1));
+            top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t tl = top & 0xFFFFu, th = top >> 16, rl = rest & 0xFFFFu, rh = rest >> 16;
+            const bool inl = rl != 0 && rl + 26u >= tl, inh = rh != 0 && rh + 26u >= th;
+            // fp16 2^(13 + e - top): exponent field 28 + e - top
+            const uint32_t fl = !inl ? 0u : rl == 256u ? 0x7E00u : (28u + rl - tl) << 10;
+            const uint32_t fh = !inh ? 0u : rh == 256u ? 0x7E00u : (28u + rh - th) << 10;
+            float d[NT][4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t sl = w < 2 ? l0 : l1, sh = w < 2 ? h0 : h1;
-              const uint32_t a0 = h2_mul(e2m1x2_of_byte<0>(wl[w]), sl), a2 = h2_mul(e2m1x2_of_byte<1>(wl[w]), sl);
-              const uint32_t b0 = h2_mul(e2m1x2_of_byte<2>(wl[w]), sl), b2 = h2_mul(e2m1x2_of_byte<3>(wl[w]), sl);
-              const uint32_t a1 = h2_mul(e2m1x2_of_byte<0>(wh[w]), sh), a3 = h2_mul(e2m1x2_of_byte<1>(wh[w]), sh);
-              const uint32_t b1 = h2_mul(e2m1x2_of_byte<2>(wh[w]), sh), b3 = h2_mul(e2m1x2_of_byte<3>(wh[w]), sh);
+            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+            mmas(fl * 0x10001u, fl * 0x10001u, fh * 0x10001u, fh * 0x10001u, d);
+            // 2^(top - 127 - 13) in two factors: it may lie outside fp32's normal range
+            const float ml = e8m0_f32(min(254u, max(tl, 1u) - 1u)), mh = e8m0_f32(min(254u, max(th, 1u) - 1u));
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
-                mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
-                mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
-              }
+            for (int n = 0; n < NT; ++n) {
+              acc[n][0] = fmaf(d[n][0] * 0x1p-13f, ml, acc[n][0]);
+              acc[n][1] = fmaf(d[n][1] * 0x1p-13f, ml, acc[n][1]);
+              acc[n][2] = fmaf(d[n][2] * 0x1p-13f, mh, acc[n][2]);
+              acc[n][3] = fmaf(d[n][3] * 0x1p-13f, mh, acc[n][3]);
             }
+            rest = (inl ? 0u : rl) | ((inh ? 0u : rh) << 16);
           };
-          if (FMT == GEMM_NVFP4) {
-            const uint32_t fl = tc_e4m3x2(s[0] & 0x7F7Fu), fh = tc_e4m3x2((s[0] >> 16) & 0x7F7Fu);
-            products(prmt_b32(fl, fl, 0x1010), prmt_b32(fl, fl, 0x3232), prmt_b32(fh, fh, 0x1010),
-                     prmt_b32(fh, fh, 0x3232), acc);
-          } else {
-            // a block whose codes are all zero counts for none (a NaN scale does)
-            uint32_t rest = s[0];  // scale bytes of the blocks still to be taken, + 1, row g's in the low half
-            {
-              const uint32_t el = s[0] & 0xFFFFu, eh = s[0] >> 16;
-              const bool zl = ((wl[0] | wl[1] | wl[2] | wl[3]) & 0x77777777u) == 0 && el != 255u;
-              const bool zh = ((wh[0] | wh[1] | wh[2] | wh[3]) & 0x77777777u) == 0 && eh != 255u;
-              rest = (zl ? 0u : el + 1u) | (zh ? 0u : (eh + 1u) << 16);
-            }
+          turn();
 #pragma unroll 1
-            while (__any_sync(0xffffffffu, rest != 0)) {
-              // the rows' largest scales among them, and the blocks within 2^-26 of those
-              uint32_t top = max_u16x2(rest, __shfl_xor_sync(0xffffffffu, rest, 1));
-              top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-              const uint32_t tl = top & 0xFFFFu, th = top >> 16, rl = rest & 0xFFFFu, rh = rest >> 16;
-              const bool inl = rl != 0 && rl + 26u >= tl, inh = rh != 0 && rh + 26u >= th;
-              // fp16 2^(13 + e - top): exponent field 28 + e - top
-              const uint32_t fl = !inl ? 0u : rl == 256u ? 0x7E00u : (28u + rl - tl) << 10;
-              const uint32_t fh = !inh ? 0u : rh == 256u ? 0x7E00u : (28u + rh - th) << 10;
-              float d[NT][4];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-              products(fl * 0x10001u, fl * 0x10001u, fh * 0x10001u, fh * 0x10001u, d);
-              // 2^(top - 127 - 13) in two factors: it may lie outside fp32's normal range
-              const float ml = e8m0_f32(min(254u, max(tl, 1u) - 1u)), mh = e8m0_f32(min(254u, max(th, 1u) - 1u));
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(d[n][0] * 0x1p-13f, ml, acc[n][0]);
-                acc[n][1] = fmaf(d[n][1] * 0x1p-13f, ml, acc[n][1]);
-                acc[n][2] = fmaf(d[n][2] * 0x1p-13f, mh, acc[n][2]);
-                acc[n][3] = fmaf(d[n][3] * 0x1p-13f, mh, acc[n][3]);
-              }
-              rest = (inl ? 0u : rl) | ((inh ? 0u : rh) << 16);
-            }
-          }
+          while (__any_sync(0xffffffffu, rest != 0)) turn();
         }
       }
+    };
+const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 1024u ? ring : p + 1024u; };
+    uint32_t take = ring;
+    bool begun = j == 0;  // the unit in hand, by this warp
+    float acc[NT][4], acc2[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[n][q] = acc2[n][q] = 0.f;
+#pragma unroll 1
+    while (at < end) {
+      // one group a step was committed up to kVecDepth steps ahead: these two have landed
+      asm volatile("cp.async.wait_group %0;" ::"n"(kVecDepth - 2) : "memory");
+      const uint32_t take2 = advance(take);
+      const uint4 l0 = ld_shared_v4(take), h0 = ld_shared_v4(take + 512);
+      const Scales s0 = r0;
+      if (j + 1 < S && at + 1 < end) {
+        const uint4 l1 = ld_shared_v4(take2), h1 = ld_shared_v4(take2 + 512);
+        const Scales s1 = r1;
+        if (at + 2 < end) load_scales(r0);
+        if (at + 3 < end) load_scales(r1);
+        products(j, l0, h0, s0, acc);
+        products(j + 1, l1, h1, s1, acc2);
+        take = advance(take2);
+        at += 2;
+        j += 2;
+        if (todo < end) { request(); ++todo; }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      } else {
+        r0 = r1;
+        if (at + 2 < end) load_scales(r1);
+        products(j, l0, h0, s0, acc);
+        take = take2;
+        ++at;
+        ++j;
+      }
+      if (todo < end) { request(); ++todo; }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (j < S && at < end) continue;
       // rows g and g + 8, columns 8 n + 2 c (+ 1): the CTA's result of the unit, or the warp's share
-      const bool whole = ja == 0 && jb == S;
+      const bool whole = begun && j == S;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int m = 8 * n + 2 * c + (q & 1), r = g + (q >> 1) * 8;
-          const float y = acc[n][q] * rscale[m] * gmul;
+          const float y = (acc[n][q] + acc2[n][q]) * rscale[m] * gmul;
+          acc[n][q] = acc2[n][q] = 0.f;
           // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
           if (!whole) {
-            part[2 * warp + (ja == 0)][r][m] = y;
+            part[2 * warp + begun][r][m] = y;
           } else if (a.split > 1) {
             sums[u][r][m] = y;
           } else if (m < rows && nb0 + u * 16 + r < N) {
             a.Y[int64_t(row + m) * N + nb0 + u * 16 + r] = uint16_t(pack_bf16x2(y, y));
           }
         }
-      at += jb - ja;
       ++u;
-      ja = 0;
-      if (at < end) {
-        open(u, 0);
-        fill(0, min(S, end - at));
-        load_scales(0);
-      }
+      j = 0;
+      begun = true;
     }
     __syncthreads();
     // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
     const int s0 = first_of(warp), us = s0 / S, ub = us * S;  // the unit of the warp's first step, and that unit's first
     if (s0 < end && s0 > ub && end >= ub + S) {
+      float y[4 * NT];  // outputs lane + 32 q of the unit's [16][8 NT]
+#pragma unroll
+      for (int q = 0; q < 4 * NT; ++q) y[q] = 0.f;
       int v = warp - 1;
       while (first_of(v) > ub) --v;
-      for (int i = lane; i < 16 * 8 * NT; i += 32) {
-        const int r = i & 15, m = i >> 4;
-        float y = 0.f;
-        for (int w = v; w <= warp; ++w)
-          if (first_of(w) < first_of(w + 1)) y += part[2 * w + (first_of(w) <= ub)][r][m];
+#pragma unroll 1
+      for (; v <= warp; ++v) {
+        const int b0 = first_of(v);
+        if (b0 == first_of(v + 1)) continue;
+        const float* share = &part[2 * v + (b0 <= ub)][0][lane % (8 * NT)] + lane / (8 * NT) * (8 * NT);
+#pragma unroll
+        for (int q = 0; q < 4 * NT; ++q) y[q] += share[32 * q];
+      }
+#pragma unroll
+      for (int q = 0; q < 4 * NT; ++q) {
+        const int r = (lane + 32 * q) / (8 * NT), m = lane % (8 * NT);
         if (a.split > 1) {
-          sums[us][r][m] = y;
+          sums[us][r][m] = y[q];
         } else if (m < rows && nb0 + us * 16 + r < N) {
-          a.Y[int64_t(row + m) * N + nb0 + us * 16 + r] = uint16_t(pack_bf16x2(y, y));
+          a.Y[int64_t(row + m) * N + nb0 + us * 16 + r] = uint16_t(pack_bf16x2(y[q], y[q]));
         }
       }
     }
@@ -1169,8 +1241,11 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
         const int r = i & 15, m = (i >> 4) % (8 * NT), uu = i / (128 * NT);
         if (m >= rows || nb0 + uu * 16 + r >= N) continue;
         const uint32_t at_sum = smem_u32(&sums[uu][r][m]);
-        float y = 0.f;
-        for (int k = 0; k < a.split; ++k) y += ld_shared_cluster_f32(map_shared_rank(at_sum, uint32_t(k)));
+        float v[8], y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < a.split ? ld_shared_cluster_f32(map_shared_rank(at_sum, uint32_t(k))) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y += v[k];
         a.Y[int64_t(row + m) * N + nb0 + uu * 16 + r] = uint16_t(pack_bf16x2(y, y));
       }
       cluster_sync();  // the sums stay until every rank has read them

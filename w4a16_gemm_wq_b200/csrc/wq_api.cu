@@ -634,24 +634,24 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
 
 // The mma.sync form for few rows per expert.  CTAs of a cluster that share K: as many as it
 // takes for a tile's rows to fit shared memory (0: more than a portable cluster).
-template <int NT>
+template <int FMT, int NT>
 int expert_gemv_split(int64_t K) {
   const int64_t steps = (K + 127) / 128;
   for (int sp = 1; sp <= 8; sp *= 2)
-    if ((steps + sp - 1) / sp <= wq::VecShape<NT>::MAX_STEPS) return sp;
+    if ((steps + sp - 1) / sp <= wq::VecShape<FMT, NT>::MAX_STEPS) return sp;
   return 0;
 }
 
 template <int FMT, int G, int NT, bool FULL>
 int launch_expert_gemv_full(wq::ExpertArgs a, cudaStream_t st) {
-  using V = wq::VecShape<NT>;
+  using V = wq::VecShape<FMT, NT>;
   const int64_t holders = std::min(a.E, a.T);
   const int64_t units = (holders + a.T / (8 * NT)) * ((int64_t(a.N) + 15) / 16);
   static std::atomic<uint64_t> attr_done{0};
   if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT, FULL>, V::OFF_X + V::MAX_STEPS * V::STEP_BYTES,
                                &attr_done, "expert gemv smem attribute"))
     return e;
-  a.split = expert_gemv_split<NT>(a.K);
+  a.split = expert_gemv_split<FMT, NT>(a.K);
   const int64_t steps = (a.K + 127) / 128;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas / a.split) * a.split), 1, 1);
@@ -683,11 +683,12 @@ int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
 
 // Tiles of 8 rows of X, or of 16 where an expert has more (5 on average already leaves
 // many above 8); false: not served.
+template <int FMT>
 bool expert_gemv_serves(const wq::ExpertArgs& a, bool* wide) {
   const int64_t holders = std::min(a.E, a.T);
   if (a.T > 16 * holders) return false;
   *wide = a.E == 1 ? a.T > 8 : a.T > 5 * holders;
-  return (*wide ? expert_gemv_split<2>(a.K) : expert_gemv_split<1>(a.K)) > 0;
+  return (*wide ? expert_gemv_split<FMT, 2>(a.K) : expert_gemv_split<FMT, 1>(a.K)) > 0;
 }
 
 template <int FMT, int G>
@@ -738,7 +739,7 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   // to hold several
   if (a.offsets ? a.T <= kExpertRowsMax : a.T <= 2) return launch_expert_rows<FMT>(v, st);
   bool wide = false;
-  if (expert_gemv_serves(a, &wide)) return launch_expert_gemv<FMT>(v, wide, st);
+  if (expert_gemv_serves<FMT>(a, &wide)) return launch_expert_gemv<FMT>(v, wide, st);
   const int64_t n = items(64);
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
   const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
