@@ -24,7 +24,7 @@
 //                and zero points of the codes' rows by cp.async, two segments deep
 //   warps 4-19   dequantizers: four groups of four warps, one 64-wide k-block of
 //                every chunk of 256 k each, into 32 columns of tensor memory
-//   warps 20-23  epilogue: tcgen05.ld, transpose in shared memory, store Y
+//   warps 20-23  epilogue: tcgen05.ld, store Y
 // All waits are bounded; see warp_wait.
 #pragma once
 
@@ -127,8 +127,7 @@ struct ExpShape {
   static constexpr int SLOT_BYTES = SK * XT * 128;
   static constexpr int OFF_X = WS * CODE_BYTES;
   static constexpr int OFF_META = OFF_X + XS * SLOT_BYTES;
-  static constexpr int OFF_STAGE = OFF_META + 2 * META_BYTES;
-  static constexpr int OFF_TAB = OFF_STAGE + 4 * 1024;
+  static constexpr int OFF_TAB = OFF_META + 2 * META_BYTES;
   static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxExperts + 4) * 4;
   static constexpr int NBAR = 2 * WS + 2 * XS + AS + 2 * NACC + 4;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 64 + 1024;
@@ -355,7 +354,8 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     return it;
   };
   // stages of a chunk: whole ones, the k-blocks past K are zeros (of the codes, the scales and X)
-  const auto stages_of = [&](int c) { return min(4 / SK, (a.K - c * kExpChunk + 64 * SK - 1) / (64 * SK)); };
+  const int last_stages = (a.K - (nchunks - 1) * kExpChunk + 64 * SK - 1) / (64 * SK);
+  const auto stages_of = [&](int c) { return c == nchunks - 1 ? last_stages : 4 / SK; };
   // a row's scale bytes, those of a chunk, and the alignment that all rows share
   const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
   const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
@@ -544,9 +544,11 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     const uint32_t piece0 = uint32_t(((2 * kb) ^ (trow & 7)) << 4), piece1 = uint32_t(((2 * kb + 1) ^ (trow & 7)) << 4);
     // byte within a row's chunk where this k-block's scales start
     const int sc_at = FMT == GEMM_INT4 ? ((kb * 64) >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 4 * kb : 2 * kb;
-    int s = 0, as = 0, ms = 0;  // stage of the codes; stage of dequantized weights; slot whose MMAs free it
+    // stage of the codes; stage of dequantized weights; slot whose MMAs free it: that of stage q - AS
+    // (counted from -AS: the slots of stages before the first are not waited for)
+    int s = 0, as = 0, ms = (kb / SK - AS + XS) % XS;
     int sg = 0;                 // segments of scales so far
-    uint32_t wpar = 0, mpar = 0;
+    uint32_t wpar = 0, mpar = kb / SK - AS < 0 ? 1 : 0;
     int q = kb / SK;            // this group's stage number; the first AS stages are free from the start
     bool ok = true;
     as = q % AS;
@@ -635,13 +637,12 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
         }
         if (++cs == cps) cs = 0;
         if (cs == 0 || c == c1 - 1) ++sg;
-        // stages up to this group's place in the next chunk
-        for (int j = 0; j < nst; ++j) {
-          if (++as == AS) as = 0;
-          if (q++ >= AS && ++ms == XS) {
-            ms = 0;
-            mpar ^= 1u;
-          }
+        q += nst;  // this group's stage in the next chunk
+        as = q % AS;
+        ms += nst;
+        if (ms >= XS) {
+          ms -= XS;
+          mpar ^= 1u;
         }
         if (++s == WS) {
           s = 0;
@@ -653,8 +654,6 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3;
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
-    const bool vec = (a.N & 7) == 0;
-    uint8_t* stage = smem + S::OFF_STAGE + quarter * 1024;  // 16 rows of X x 32 weight rows, bf16
     int i = 0;
     for (int id = first; id < items; id += step, ++i) {
       const Item it = item_of(id);
@@ -662,7 +661,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const float gmul = FMT == GEMM_NVFP4 ? __ldg(a.gscale + it.e) : FMT == GEMM_INT4 ? 0.0625f : 1.0f;
       if (!warp_wait(&dfull[b], u & 1, ERR_TIMEOUT_MMA, abort_flag)) break;
       tc_fence_after();
-      const int nw = it.n0 + quarter * 32;  // this warp's first weight row
+      const int n = it.n0 + quarter * 32 + lane;  // this lane's weight row
       for (int x = 0; x < it.rows; x += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + lane_base + uint32_t(b * XT + x), v);
@@ -675,34 +674,16 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
             if (x + j < it.rows) part[(x + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]) * gmul;
           continue;
         }
-        if (!vec) {
-          const int n = nw + lane;
-          if (n < a.N) {
+        // a row of X at a time: 32 lanes' weight rows are 64 bytes of Y's row, whole sectors
+        if (n < a.N) {
+          uint16_t* y = a.Y + int64_t(it.row + x) * a.N + n;
+          const int left = it.rows - x;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (x + j < it.rows) {
-                const float y = __uint_as_float(v[j]) * gmul;
-                a.Y[int64_t(it.row + x + j) * a.N + n] = uint16_t(pack_bf16x2(y, y));
-              }
-          }
-          continue;
-        }
-#pragma unroll
-        for (int h = 0; h < 32; h += 16) {  // 16 rows of X: transpose, then 16-byte pieces of Y's rows
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const uint32_t y2 = pack_bf16x2(__uint_as_float(v[h + j]) * gmul, __uint_as_float(v[h + j + 1]) * gmul);
-            *reinterpret_cast<uint16_t*>(stage + j * 64 + lane * 2) = uint16_t(y2);
-            *reinterpret_cast<uint16_t*>(stage + (j + 1) * 64 + lane * 2) = uint16_t(y2 >> 16);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int p = 0; p < 16; p += 8) {
-            const int j = p + (lane >> 2), n = nw + (lane & 3) * 8;
-            if (x + h + j < it.rows && n < a.N)
-              *reinterpret_cast<uint4*>(a.Y + int64_t(it.row + x + h + j) * a.N + n) =
-                  *reinterpret_cast<const uint4*>(stage + j * 64 + (lane & 3) * 16);
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t y2 = pack_bf16x2(__uint_as_float(v[j]) * gmul, __uint_as_float(v[j + 1]) * gmul);
+            if (j < left) y[0] = uint16_t(y2);
+            if (j + 1 < left) y[a.N] = uint16_t(y2 >> 16);
+            y += 2 * int64_t(a.N);
           }
         }
       }
