@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: mma.sync with the weights (16 rows of W_e) as the A operand,
-// dequantized in registers, and up to 8 NT rows of X as B, both in fp16.  Bound by HBM
+// dequantized in registers, and up to 8 rows of X as B, both in fp16.  Bound by HBM
 // (0.53 to 0.63 bytes a weight) and by the instructions of the dequantization, which
 // is why both operands are fp16: a pair of E2M1 codes is one conversion and one product
 // there, against one conversion, two multiply-adds and a packing in bf16.
@@ -754,19 +754,20 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 //          the step's fp32 sums times that one; blocks under 2^-26 of it take another turn.
 constexpr int kVecWarps = 16;
 constexpr int kVecDepth = 6;
+constexpr int kVecRows = 8;  // rows of X of a tile
 constexpr int kVecRing = kVecWarps * kVecDepth * 1024;
 
 // Shared memory: codes [warp][kVecDepth][2][32 lanes][16 bytes], the CTA's sums of a run of units
 // (where a cluster shares them), sums of units that straddle warps, X fragments.
-template <int FMT, int NT>
+template <int FMT>
 struct VecShape {
-  static constexpr int SUM_BYTES = 16 * 8 * NT * 4;              // one unit's sums
-  static constexpr int MAX_UNITS = 16 / NT;
+  static constexpr int SUM_BYTES = 16 * 8 * 4;                   // one unit's sums
+  static constexpr int MAX_UNITS = 16;
   static constexpr int OFF_SUMS = kVecRing;
   static constexpr int OFF_PART = OFF_SUMS + MAX_UNITS * SUM_BYTES;
   static constexpr int OFF_X = OFF_PART + 2 * kVecWarps * SUM_BYTES;
-  static constexpr int FRAG_BYTES = NT * 2048;                   // X fragments of a step
-  static constexpr int STEP_BYTES = FRAG_BYTES + (FMT == GEMM_INT4 ? NT * 256 : 0);  // and P, Q of its groups
+  static constexpr int FRAG_BYTES = 2048;                        // X fragments of a step
+  static constexpr int STEP_BYTES = FRAG_BYTES + (FMT == GEMM_INT4 ? 256 : 0);  // and P, Q of its groups
   static constexpr int MAX_STEPS = (216 * 1024 - OFF_X) / STEP_BYTES;
 };
 
@@ -778,29 +779,29 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 // FULL: K % 128 == 0, no step reaches past K (and a step's scales of a row are aligned words).
-template <int FMT, int G, int NT, bool FULL>
+template <int FMT, int G, bool FULL>
 __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __grid_constant__ ExpertArgs a) {
   static_assert(FMT != GEMM_INT4 || G == 32 || G == 64 || G == 128, "group size");
-  using V = VecShape<FMT, NT>;
+  using V = VecShape<FMT>;
   constexpr int NG = FMT == GEMM_INT4 ? 128 / G : 1;    // groups of a step
   constexpr int WPG = 4 / NG;                           // words (8 k) of a lane per group
   extern __shared__ __align__(1024) uint8_t vec_smem[];
   __shared__ int bound[kMaxExperts + 4], tstart[kMaxExperts + 4];
   __shared__ int bad_flag;
-  __shared__ uint32_t rtop[8 * NT];                     // largest finite magnitude of X's rows, fp32 bits
-  __shared__ float rscale[8 * NT];                      // what undoes their scaling
-  float (*part)[16][8 * NT] = reinterpret_cast<float (*)[16][8 * NT]>(vec_smem + V::OFF_PART);
-  float (*sums)[16][8 * NT] = reinterpret_cast<float (*)[16][8 * NT]>(vec_smem + V::OFF_SUMS);
+  __shared__ uint32_t rtop[kVecRows];                     // largest finite magnitude of X's rows, fp32 bits
+  __shared__ float rscale[kVecRows];                      // what undoes their scaling
+  float (*part)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_PART);
+  float (*sums)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_SUMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int K = a.K, N = a.N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.offsets) {
-    if (warp == 0) expert_tables(a, 8 * NT, bound, tstart, &bad_flag);
+    if (warp == 0) expert_tables(a, kVecRows, bound, tstart, &bad_flag);
     __syncthreads();
     if (bad_flag) return;
   }
-  const int tiles = a.offsets ? tstart[a.E] : (a.T + 8 * NT - 1) / (8 * NT);
+  const int tiles = a.offsets ? tstart[a.E] : (a.T + kVecRows - 1) / kVecRows;
   const int nrb = (N + 15) >> 4;                        // row blocks of an expert
   // this cluster's units, this CTA's steps of each
   int rank = 0, cl = blockIdx.x, ncl = gridDim.x, S0 = 0, S = (K + 127) >> 7;
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     const int tile = u0 / nrb;
     int u1 = min(ulast, (tile + 1) * nrb);
     if (a.split > 1) u1 = min(u1, u0 + V::MAX_UNITS);
-    int e = 0, row = tile * 8 * NT, rows = min(8 * NT, a.T - row);
+    int e = 0, row = tile * kVecRows, rows = min(kVecRows, a.T - row);
     if (a.offsets) {
       e = expert_of_tile(tstart, a.E, tile);
       const int r = bound[e + 1] - bound[e], nt = tstart[e + 1] - tstart[e];
@@ -935,12 +936,12 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     }
     if (staged != tile) {
       // X, or X * act_inv_s, 256 k of a row at a time: the rows' largest finite magnitudes, then the fragments
-      if (threadIdx.x < 8 * NT) rtop[threadIdx.x] = 0;
+      if (threadIdx.x < kVecRows) rtop[threadIdx.x] = 0;
       __syncthreads();  // also: the last run's readers are done
       const float* f = FMT == GEMM_MXFP4 && a.inv_s ? a.inv_s + S0 * 128 : nullptr;
       const int len = min(S * 128, K - S0 * 128);
-      // each row by 2 / NT warps, alternate runs of 256 k
-      constexpr int WPR = kVecWarps / (8 * NT);
+      // each row by two warps, alternate runs of 256 k
+      constexpr int WPR = kVecWarps / kVecRows;
       const int m = warp / WPR, kend = m < rows ? S * 128 : 0;
       const uint16_t* xrow = a.X + int64_t(row + min(m, rows - 1)) * K + S0 * 128;
       // four runs' loads in flight at once, twice over (the second time from L1)
@@ -1016,13 +1017,13 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
             Q += __shfl_xor_sync(0xffffffffu, Q, h);
           }
           if (in && p * 8 % G == 0)
-            *reinterpret_cast<float2*>(step + V::FRAG_BYTES + ((p * 8 / G) * 8 * NT + m) * 8) = make_float2(P, Q);
+            *reinterpret_cast<float2*>(step + V::FRAG_BYTES + ((p * 8 / G) * kVecRows + m) * 8) = make_float2(P, Q);
         } else {
           cc = p >> 2;
           w = p & 3;
           o = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
         }
-        if (in) *reinterpret_cast<uint4*>(step + (m >> 3) * 2048 + w * 512 + (4 * (m & 7) + cc) * 16) = o;
+        if (in) *reinterpret_cast<uint4*>(step + w * 512 + (4 * m + cc) * 16) = o;
       });
       staged = tile;
       __syncthreads();
@@ -1030,12 +1031,12 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 
     // ---- the warp's steps
     // one step's products from its codes, scales and fragments
-    const auto products = [&](int j, const uint4& cl4, const uint4& ch4, const Scales& r, float (&acc)[NT][4]) {
+    const auto products = [&](int j, const uint4& cl4, const uint4& ch4, const Scales& r, float (&acc)[4]) {
       const uint32_t wl[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, wh[4] = {ch4.x, ch4.y, ch4.z, ch4.w};
       const uint32_t xs = xfrag + uint32_t(j * V::STEP_BYTES);
       if (FMT == GEMM_INT4) {
         const uint32_t pq = smem_u32(vec_smem) + uint32_t(V::OFF_X + V::FRAG_BYTES + j * V::STEP_BYTES + c * 16);
-        float d[NT][4];  // the group's sums
+        float d[4];  // the group's sums
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           constexpr uint32_t B = 0x64006400u;  // fp16 1024: a code under it is 1024 + q (or + 16 q)
@@ -1044,13 +1045,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           const uint32_t a1 = lop3_andor(wh[w], 0x000F000Fu, B), a3 = lop3_andor(wh[w], 0x00F000F0u, B);
           const uint32_t b0 = lop3_andor(l8, 0x000F000Fu, B), b2 = lop3_andor(l8, 0x00F000F0u, B);
           const uint32_t b1 = lop3_andor(h8, 0x000F000Fu, B), b3 = lop3_andor(h8, 0x00F000F0u, B);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
-            if (w % WPG == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-            mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
-            mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
-          }
+          const uint4 x = ld_shared_v4(xs + uint32_t(w * 512));
+          if (w % WPG == 0) d[0] = d[1] = d[2] = d[3] = 0.f;
+          mma_f16_16816(d, a0, a1, a2, a3, x.x, x.y);
+          mma_f16_16816(d, b0, b1, b2, b3, x.z, x.w);
           if (w % WPG == WPG - 1) {
             const int gi = w / WPG, nib = 4 * ((G == 128 ? ((S0 + j) & 1) : 0) + gi);
             const bool words = FULL && NG > 1;
@@ -1059,21 +1057,18 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s2));
             const float zl = __uint_as_float(lop3_andor(r.zl >> nib, 15u, 0x4B000000u)) - 8388608.f;
             const float zh = __uint_as_float(lop3_andor(r.zh >> nib, 15u, 0x4B000000u)) - 8388608.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 t = ld_shared_v4(pq + uint32_t((gi * NT + n) * 64));  // P, Q of columns 2 c and 2 c + 1
-              const float P0 = __uint_as_float(t.x), Q0 = __uint_as_float(t.y);
-              const float P1 = __uint_as_float(t.z), Q1 = __uint_as_float(t.w);
-              acc[n][0] = fmaf(f.x, fmaf(-zl, Q0, d[n][0] - P0), acc[n][0]);
-              acc[n][1] = fmaf(f.x, fmaf(-zl, Q1, d[n][1] - P1), acc[n][1]);
-              acc[n][2] = fmaf(f.y, fmaf(-zh, Q0, d[n][2] - P0), acc[n][2]);
-              acc[n][3] = fmaf(f.y, fmaf(-zh, Q1, d[n][3] - P1), acc[n][3]);
-            }
+            const uint4 t = ld_shared_v4(pq + uint32_t(gi * 64));  // P, Q of columns 2 c and 2 c + 1
+            const float P0 = __uint_as_float(t.x), Q0 = __uint_as_float(t.y);
+            const float P1 = __uint_as_float(t.z), Q1 = __uint_as_float(t.w);
+            acc[0] = fmaf(f.x, fmaf(-zl, Q0, d[0] - P0), acc[0]);
+            acc[1] = fmaf(f.x, fmaf(-zl, Q1, d[1] - P1), acc[1]);
+            acc[2] = fmaf(f.y, fmaf(-zh, Q0, d[2] - P0), acc[2]);
+            acc[3] = fmaf(f.y, fmaf(-zh, Q1, d[3] - P1), acc[3]);
           }
         }
       } else {
         // A = code times scale; fp16 pairs of the lane's two NVFP4 blocks, or of its MXFP4 block
-        const auto mmas = [&](uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1, float (&d)[NT][4]) {
+        const auto mmas = [&](uint32_t l0, uint32_t l1, uint32_t h0, uint32_t h1, float (&d)[4]) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t sl = w < 2 ? l0 : l1, sh = w < 2 ? h0 : h1;
@@ -1081,12 +1076,9 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
             const uint32_t b0 = h2_mul(e2m1x2_of_byte<2>(wl[w]), sl), b2 = h2_mul(e2m1x2_of_byte<3>(wl[w]), sl);
             const uint32_t a1 = h2_mul(e2m1x2_of_byte<0>(wh[w]), sh), a3 = h2_mul(e2m1x2_of_byte<1>(wh[w]), sh);
             const uint32_t b1 = h2_mul(e2m1x2_of_byte<2>(wh[w]), sh), b3 = h2_mul(e2m1x2_of_byte<3>(wh[w]), sh);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 x = ld_shared_v4(xs + uint32_t(n * 2048 + w * 512));
-              mma_f16_16816(d[n], a0, a1, a2, a3, x.x, x.y);
-              mma_f16_16816(d[n], b0, b1, b2, b3, x.z, x.w);
-            }
+            const uint4 x = ld_shared_v4(xs + uint32_t(w * 512));
+            mma_f16_16816(d, a0, a1, a2, a3, x.x, x.y);
+            mma_f16_16816(d, b0, b1, b2, b3, x.z, x.w);
           }
         };
         if (FMT == GEMM_NVFP4) {
@@ -1108,19 +1100,14 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
             // fp16 2^(13 + e - top): exponent field 28 + e - top
             const uint32_t fl = !inl ? 0u : rl == 256u ? 0x7E00u : (28u + rl - tl) << 10;
             const uint32_t fh = !inh ? 0u : rh == 256u ? 0x7E00u : (28u + rh - th) << 10;
-            float d[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
             mmas(fl * 0x10001u, fl * 0x10001u, fh * 0x10001u, fh * 0x10001u, d);
             // 2^(top - 127 - 13) in two factors: it may lie outside fp32's normal range
             const float ml = e8m0_f32(min(254u, max(tl, 1u) - 1u)), mh = e8m0_f32(min(254u, max(th, 1u) - 1u));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[n][0] = fmaf(d[n][0] * 0x1p-13f, ml, acc[n][0]);
-              acc[n][1] = fmaf(d[n][1] * 0x1p-13f, ml, acc[n][1]);
-              acc[n][2] = fmaf(d[n][2] * 0x1p-13f, mh, acc[n][2]);
-              acc[n][3] = fmaf(d[n][3] * 0x1p-13f, mh, acc[n][3]);
-            }
+            acc[0] = fmaf(d[0] * 0x1p-13f, ml, acc[0]);
+            acc[1] = fmaf(d[1] * 0x1p-13f, ml, acc[1]);
+            acc[2] = fmaf(d[2] * 0x1p-13f, mh, acc[2]);
+            acc[3] = fmaf(d[3] * 0x1p-13f, mh, acc[3]);
             rest = (inl ? 0u : rl) | ((inh ? 0u : rh) << 16);
           };
           turn();
@@ -1129,14 +1116,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
         }
       }
     };
-const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 1024u ? ring : p + 1024u; };
+    const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 1024u ? ring : p + 1024u; };
     uint32_t take = ring;
     bool begun = j == 0;  // the unit in hand, by this warp
-    float acc[NT][4], acc2[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[n][q] = acc2[n][q] = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     while (at < end) {
       // one group a step was committed up to kVecDepth steps ahead: these two have landed
@@ -1167,24 +1150,22 @@ const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 10
       if (todo < end) { request(); ++todo; }
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (j < S && at < end) continue;
-      // rows g and g + 8, columns 8 n + 2 c (+ 1): the CTA's result of the unit, or the warp's share
+      // rows g and g + 8, columns 2 c and 2 c + 1: the CTA's result of the unit, or the warp's share
       const bool whole = begun && j == S;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int m = 8 * n + 2 * c + (q & 1), r = g + (q >> 1) * 8;
-          const float y = (acc[n][q] + acc2[n][q]) * rscale[m] * gmul;
-          acc[n][q] = acc2[n][q] = 0.f;
-          // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
-          if (!whole) {
-            part[2 * warp + begun][r][m] = y;
-          } else if (a.split > 1) {
-            sums[u][r][m] = y;
-          } else if (m < rows && nb0 + u * 16 + r < N) {
-            a.Y[int64_t(row + m) * N + nb0 + u * 16 + r] = uint16_t(pack_bf16x2(y, y));
-          }
+      for (int q = 0; q < 4; ++q) {
+        const int m = 2 * c + (q & 1), r = g + (q >> 1) * 8;
+        const float y = (acc[q] + acc2[q]) * rscale[m] * gmul;
+        acc[q] = acc2[q] = 0.f;
+        // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
+        if (!whole) {
+          part[2 * warp + begun][r][m] = y;
+        } else if (a.split > 1) {
+          sums[u][r][m] = y;
+        } else if (m < rows && nb0 + u * 16 + r < N) {
+          a.Y[int64_t(row + m) * N + nb0 + u * 16 + r] = uint16_t(pack_bf16x2(y, y));
         }
+      }
       ++u;
       j = 0;
       begun = true;
@@ -1193,22 +1174,20 @@ const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 10
     // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
     const int s0 = first_of(warp), us = s0 / S, ub = us * S;  // the unit of the warp's first step, and that unit's first
     if (s0 < end && s0 > ub && end >= ub + S) {
-      float y[4 * NT];  // outputs lane + 32 q of the unit's [16][8 NT]
-#pragma unroll
-      for (int q = 0; q < 4 * NT; ++q) y[q] = 0.f;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};  // outputs lane + 32 q of the unit's [16][8]
       int v = warp - 1;
       while (first_of(v) > ub) --v;
 #pragma unroll 1
       for (; v <= warp; ++v) {
         const int b0 = first_of(v);
         if (b0 == first_of(v + 1)) continue;
-        const float* share = &part[2 * v + (b0 <= ub)][0][lane % (8 * NT)] + lane / (8 * NT) * (8 * NT);
+        const float* share = &part[2 * v + (b0 <= ub)][0][0] + lane;
 #pragma unroll
-        for (int q = 0; q < 4 * NT; ++q) y[q] += share[32 * q];
+        for (int q = 0; q < 4; ++q) y[q] += share[32 * q];
       }
 #pragma unroll
-      for (int q = 0; q < 4 * NT; ++q) {
-        const int r = (lane + 32 * q) / (8 * NT), m = lane % (8 * NT);
+      for (int q = 0; q < 4; ++q) {
+        const int r = (lane + 32 * q) >> 3, m = lane & 7;
         if (a.split > 1) {
           sums[us][r][m] = y[q];
         } else if (m < rows && nb0 + us * 16 + r < N) {
@@ -1218,8 +1197,8 @@ const auto advance = [&](uint32_t p) { return p + 1024u == ring + kVecDepth * 10
     }
     if (a.split > 1) {
       cluster_sync();  // every CTA of the cluster has its sums in shared memory
-      for (int i = rank * int(blockDim.x) + threadIdx.x; i < (u1 - u0) * 128 * NT; i += a.split * int(blockDim.x)) {
-        const int r = i & 15, m = (i >> 4) % (8 * NT), uu = i / (128 * NT);
+      for (int i = rank * int(blockDim.x) + threadIdx.x; i < (u1 - u0) * 128; i += a.split * int(blockDim.x)) {
+        const int r = i & 15, m = (i >> 4) & 7, uu = i >> 7;
         if (m >= rows || nb0 + uu * 16 + r >= N) continue;
         const uint32_t at_sum = smem_u32(&sums[uu][r][m]);
         float v[8], y = 0.f;
@@ -1255,7 +1234,8 @@ template <int FMT, int MT>
 __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
     expert_row_kernel(const __grid_constant__ ExpertArgs a, int ksplit) {
   __shared__ float part[kRowWarps][kRowRows * MT];
-  extern __shared__ __align__(16) uint8_t row_smem[];  // codes: [2][warp][row][32 lanes][16 bytes]
+  // codes: [2][warp][row][32 lanes][16 bytes]; with 1/s, a run's 1024 of it: [warp][4096 bytes]
+  extern __shared__ __align__(16) uint8_t row_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % ksplit, rb = blockIdx.x * (kRowWarps / ksplit) + warp / ksplit;
   const int n0 = rb * kRowRows, i0 = blockIdx.y;  // first weight row, first row of X
@@ -1298,7 +1278,22 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
         cp_async_zfill<16>(dst + r * 512, in ? p + min(r, last) * int64_t(K >> 1) : a.packed, in ? 16 : 0);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // 1/s of a run, loaded along K: 32 lanes that each read 128 bytes in a row would touch 32
+    // lines a load.  Piece c of lane l's eight lies at c ^ (l & 7), so that the reads spread over
+    // the banks too.
+    const uint32_t fslot = smem_u32(row_smem) + uint32_t(2 * kRowWarps * kRowRows * 512 + warp * 4096);
+    const bool scaled = FMT == GEMM_MXFP4 && a.inv_s;
+    const auto request_inv = [&](int k0) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = q * 32 + lane;  // piece of four
+        const bool in = k0 + 4 * i < K;
+        cp_async_zfill<16>(fslot + uint32_t((i & ~7) + ((i ^ (i >> 3)) & 7)) * 16, in ? a.inv_s + k0 + 4 * i : a.inv_s, in ? 16 : 0);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     uint32_t slot = slots;
+    if (scaled) request_inv(sub * 1024);
     request(sub * 1024, slot);
 #pragma unroll 1
     for (int k0 = sub * 1024; k0 < K; k0 += ksplit * 1024) {
@@ -1309,8 +1304,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
       } else {
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
+      if (scaled) {  // groups under way: 1/s and codes of the first run, or the other way round of a later one; the next codes
+        if (k0 == sub * 1024)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+      }
       const int k = k0 + lane * 32;
-      if (k >= K) break;
+      if (k >= K) break;  // only in a warp's last run
       // raw scales and zero-point words: nothing waits for them yet
       uint32_t sc[kRowRows], zp[kRowRows];
       {
@@ -1340,24 +1342,31 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const bool scaled = FMT == GEMM_MXFP4 && a.inv_s;
-        const auto pair = [&](int j) {  // elements 2j and 2j + 1
-          float2 f = make_float2(__uint_as_float(xh[m][j] << 16), __uint_as_float(xh[m][j] & 0xFFFF0000u));
+        const auto quad = [&](int j) {  // elements 4 j to 4 j + 3
+          const uint32_t u = xh[m][2 * j], v = xh[m][2 * j + 1];
+          float4 f = make_float4(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u), __uint_as_float(v << 16),
+                                 __uint_as_float(v & 0xFFFF0000u));
           if (scaled) {
-            const float2 i = __ldg(reinterpret_cast<const float2*>(a.inv_s + k + 2 * j));
-            f.x *= i.x;
-            f.y *= i.y;
+            const uint4 i = ld_shared_v4(fslot + uint32_t(lane * 8 + (j ^ (lane & 7))) * 16);
+            f.x *= __uint_as_float(i.x);
+            f.y *= __uint_as_float(i.y);
+            f.z *= __uint_as_float(i.z);
+            f.w *= __uint_as_float(i.w);
           }
           return f;
         };
         uint32_t top = 0;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 f = pair(j);
-          const uint32_t b0 = __float_as_uint(f.x) & 0x7FFFFFFFu, b1 = __float_as_uint(f.y) & 0x7FFFFFFFu;
-          top = max(top, max(b0 < 0x7F800000u ? b0 : 0u, b1 < 0x7F800000u ? b1 : 0u));
-          if (FMT == GEMM_INT4) s += f.x + f.y;
+        for (int j = 0; j < 8; ++j) {
+          const float4 f = quad(j);
+          const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+            top = max(top, b < 0x7F800000u ? b : 0u);
+            if (FMT == GEMM_INT4) s += v[i];
+          }
         }
         const uint32_t fe = min(254u, 268u - max(top >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
         const float up = __uint_as_float(fe << 23);
@@ -1365,21 +1374,31 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
         sum[m] = s;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float2 f0 = pair(4 * q), f1 = pair(4 * q + 1), f2 = pair(4 * q + 2), f3 = pair(4 * q + 3);
+          const float4 f = quad(2 * q), g = quad(2 * q + 1);
           if (FMT == GEMM_INT4) {
-            xh[m][4 * q] = pack_f16x2(f0.x * up, f2.x * up);
-            xh[m][4 * q + 1] = pack_f16x2(f0.y * up, f2.y * up);
-            xh[m][4 * q + 2] = pack_f16x2(f1.x * up, f3.x * up);
-            xh[m][4 * q + 3] = pack_f16x2(f1.y * up, f3.y * up);
+            xh[m][4 * q] = pack_f16x2(f.x * up, g.x * up);
+            xh[m][4 * q + 1] = pack_f16x2(f.y * up, g.y * up);
+            xh[m][4 * q + 2] = pack_f16x2(f.z * up, g.z * up);
+            xh[m][4 * q + 3] = pack_f16x2(f.w * up, g.w * up);
           } else {
-            xh[m][4 * q] = pack_f16x2(f0.x * up, f0.y * up);
-            xh[m][4 * q + 1] = pack_f16x2(f1.x * up, f1.y * up);
-            xh[m][4 * q + 2] = pack_f16x2(f2.x * up, f2.y * up);
-            xh[m][4 * q + 3] = pack_f16x2(f3.x * up, f3.y * up);
+            xh[m][4 * q] = pack_f16x2(f.x * up, f.y * up);
+            xh[m][4 * q + 1] = pack_f16x2(f.z * up, f.w * up);
+            xh[m][4 * q + 2] = pack_f16x2(g.x * up, g.y * up);
+            xh[m][4 * q + 3] = pack_f16x2(g.z * up, g.w * up);
           }
         }
       }
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (scaled) {
+        if (k0 + ksplit * 1024 < K) {  // then no lane has left
+          __syncwarp();                // every lane has taken this run's
+          request_inv(k0 + ksplit * 1024);
+        } else {
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      }
 #pragma unroll
       for (int r = 0; r < kRowRows; ++r) {
         const uint4 w = ld_shared_v4(here + r * 512);

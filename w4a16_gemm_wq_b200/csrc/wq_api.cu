@@ -597,8 +597,54 @@ int launch_mxf4(wq::Mxf4Args& a, const uint8_t* xcodes, const uint8_t* wcodes, c
 }
 
 // ---------------------------------------------------------------- experts
+// A launch of clusters of `split` CTAs (1: no clusters), with programmatic stream serialization.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+
+  ClusterLaunch(int threads, size_t smem, int split, cudaStream_t st) {
+    cfg.gridDim = dim3(unsigned(split), 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+  }
+  ClusterLaunch(const ClusterLaunch&) = delete;
+  ClusterLaunch& operator=(const ClusterLaunch&) = delete;
+};
+
+// How many clusters of `split` CTAs, one CTA to an SM, run at once: fewer than SMs / split,
+// since a cluster stays within a GPC (B200: 74 pairs, 33 fours, 15 eights).  Asked once per
+// kernel, device and size; `seen` (one per split) remembers the last answer.
+constexpr int kExpMaxSplit = 8;
+template <typename Kern>
+int resident_clusters(Kern kern, int threads, size_t smem, int split, std::atomic<uint64_t>* seen) {
+  if (split == 1) return wq::kTcMaxCtas;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const uint64_t key = (uint64_t(dev + 1) << 32 | uint64_t(smem)) << 16;
+  const uint64_t last = seen[split].load(std::memory_order_relaxed);
+  if ((last & ~uint64_t(0xFFFF)) == key) return int(last & 0xFFFF);
+  ClusterLaunch probe(threads, smem, split, nullptr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &probe.cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  n = std::min(n, wq::kTcMaxCtas / split);
+  seen[split].store(key | uint64_t(n), std::memory_order_relaxed);
+  return n;
+}
+
 template <int FMT, typename S>
-int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed, int split, int64_t items,
+int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed, bool splits, int64_t items,
                         cudaStream_t st) {
   if (int e = make_tmap_2d(&a.tmW, packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.E) * uint64_t(a.N),
                            uint64_t(a.K / 2), 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -609,101 +655,90 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
   static std::atomic<uint64_t> attr_done{0};
   if (int e = ensure_smem_attr(wq::expert_gemm_kernel<FMT, S>, S::SMEM_BYTES, &attr_done, "expert smem attribute"))
     return e;
-  a.split = split;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(split > 1 ? items * split : std::min<int64_t>(items, wq::kTcMaxCtas)), 1, 1);
-  cfg.blockDim = dim3(wq::kExpThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::SMEM_BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
-  if (split > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = split;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
+  // few items: K shared by a cluster.  The split that ends first, counting a launch's start and
+  // end as three chunks of K and the sum over the cluster as one
+  const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
+  a.split = 1;
+  if (splits && items < wq::kTcMaxCtas) {
+    static std::atomic<uint64_t> seen[kExpMaxSplit + 1];
+    int64_t best = chunks + 3;
+    for (int sp = 2; sp <= std::min<int64_t>(kExpMaxSplit, chunks); ++sp) {
+      const int64_t at_once = resident_clusters(wq::expert_gemm_kernel<FMT, S>, wq::kExpThreads, S::SMEM_BYTES, sp, seen);
+      const int64_t t = (items + at_once - 1) / at_once * ((chunks + sp - 1) / sp + 4);
+      if (t < best) {
+        best = t;
+        a.split = sp;
+      }
+    }
   }
-  cfg.attrs = attr;
-  cfg.numAttrs = na;
-  return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
+  ClusterLaunch l(wq::kExpThreads, S::SMEM_BYTES, a.split, st);
+  l.cfg.gridDim.x = unsigned(a.split > 1 ? items * a.split : std::min<int64_t>(items, wq::kTcMaxCtas));
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
 }
 
-// The mma.sync form for few rows per expert.  CTAs of a cluster that share K: as many as it
-// takes for a tile's rows to fit shared memory (0: more than a portable cluster).
-template <int FMT, int NT>
+// The mma.sync form for few rows per expert.  The fewest CTAs of a cluster that share K for a
+// tile's rows to fit their shared memory (0: more than a portable cluster).
+template <int FMT>
 int expert_gemv_split(int64_t K) {
-  const int64_t steps = (K + 127) / 128;
-  for (int sp = 1; sp <= 8; sp *= 2)
-    if ((steps + sp - 1) / sp <= wq::VecShape<FMT, NT>::MAX_STEPS) return sp;
-  return 0;
+  const int64_t steps = (K + 127) / 128, most = wq::VecShape<FMT>::MAX_STEPS, sp = (steps + most - 1) / most;
+  return sp <= kExpMaxSplit ? int(sp) : 0;
 }
 
-template <int FMT, int G, int NT, bool FULL>
+template <int FMT, int G, bool FULL>
 int launch_expert_gemv_full(wq::ExpertArgs a, cudaStream_t st) {
-  using V = wq::VecShape<FMT, NT>;
+  using V = wq::VecShape<FMT>;
   const int64_t holders = std::min(a.E, a.T);
-  const int64_t units = (holders + a.T / (8 * NT)) * ((int64_t(a.N) + 15) / 16);
+  const int64_t units = (holders + a.T / wq::kVecRows) * ((int64_t(a.N) + 15) / 16);
   static std::atomic<uint64_t> attr_done{0};
-  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, NT, FULL>, V::OFF_X + V::MAX_STEPS * V::STEP_BYTES,
+  if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, FULL>, V::OFF_X + V::MAX_STEPS * V::STEP_BYTES,
                                &attr_done, "expert gemv smem attribute"))
     return e;
-  a.split = expert_gemv_split<FMT, NT>(a.K);
+  // of the splits that fit, the one whose busiest CTA has the fewest steps
   const int64_t steps = (a.K + 127) / 128;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas / a.split) * a.split), 1, 1);
-  cfg.blockDim = dim3(wq::kVecWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = size_t(V::OFF_X + (steps + a.split - 1) / a.split * V::STEP_BYTES);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
-  if (a.split > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = a.split;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
+  const auto smem_of = [&](int sp) { return size_t(V::OFF_X + (steps + sp - 1) / sp * V::STEP_BYTES); };
+  const auto kern = wq::expert_gemv_kernel<FMT, G, FULL>;
+  static std::atomic<uint64_t> seen[kExpMaxSplit + 1];
+  int64_t best = INT64_MAX, clusters = 1;
+  const int least = expert_gemv_split<FMT>(a.K);
+  for (int sp = least; sp <= (least > 1 ? kExpMaxSplit : 1); ++sp) {
+    const int64_t n = std::min<int64_t>(units, resident_clusters(kern, wq::kVecWarps * 32, smem_of(sp), sp, seen));
+    const int64_t t = (units + n - 1) / n * ((steps + sp - 1) / sp);
+    if (t < best) {
+      best = t;
+      a.split = sp;
+      clusters = n;
+    }
   }
-  cfg.attrs = attr;
-  cfg.numAttrs = na;
-  return cuda_check(cudaLaunchKernelEx(&cfg, wq::expert_gemv_kernel<FMT, G, NT, FULL>, a), "expert gemv launch");
-}
-
-template <int FMT, int G, int NT>
-int launch_expert_gemv_nt(const wq::ExpertArgs& a, cudaStream_t st) {
-  return a.K % 128 == 0 ? launch_expert_gemv_full<FMT, G, NT, true>(a, st)
-                        : launch_expert_gemv_full<FMT, G, NT, false>(a, st);
-}
-
-// Tiles of 8 rows of X, or of 16 where an expert has more (5 on average already leaves
-// many above 8); false: not served.
-template <int FMT>
-bool expert_gemv_serves(const wq::ExpertArgs& a, bool* wide) {
-  const int64_t holders = std::min(a.E, a.T);
-  if (a.T > 16 * holders) return false;
-  *wide = a.E == 1 ? a.T > 8 : a.T > 5 * holders;
-  return (*wide ? expert_gemv_split<FMT, 2>(a.K) : expert_gemv_split<FMT, 1>(a.K)) > 0;
+  ClusterLaunch l(wq::kVecWarps * 32, smem_of(a.split), a.split, st);
+  l.cfg.gridDim.x = unsigned(clusters * a.split);
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, kern, a), "expert gemv launch");
 }
 
 template <int FMT, int G>
-int launch_expert_gemv_g(const wq::ExpertArgs& a, bool wide, cudaStream_t st) {
-  return wide ? launch_expert_gemv_nt<FMT, G, 2>(a, st) : launch_expert_gemv_nt<FMT, G, 1>(a, st);
+int launch_expert_gemv_g(const wq::ExpertArgs& a, cudaStream_t st) {
+  return a.K % 128 == 0 ? launch_expert_gemv_full<FMT, G, true>(a, st) : launch_expert_gemv_full<FMT, G, false>(a, st);
 }
 
 template <int FMT>
-int launch_expert_gemv(const wq::ExpertArgs& a, bool wide, cudaStream_t st) {
+int launch_expert_gemv(const wq::ExpertArgs& a, cudaStream_t st) {
   if constexpr (FMT == wq::GEMM_INT4)
-    return a.log2g == 5   ? launch_expert_gemv_g<FMT, 32>(a, wide, st)
-           : a.log2g == 6 ? launch_expert_gemv_g<FMT, 64>(a, wide, st)
-                          : launch_expert_gemv_g<FMT, 128>(a, wide, st);
+    return a.log2g == 5   ? launch_expert_gemv_g<FMT, 32>(a, st)
+           : a.log2g == 6 ? launch_expert_gemv_g<FMT, 64>(a, st)
+                          : launch_expert_gemv_g<FMT, 128>(a, st);
   else
-    return launch_expert_gemv_g<FMT, 0>(a, wide, st);
+    return launch_expert_gemv_g<FMT, 0>(a, st);
+}
+
+// Whether that form serves a call: at most 8 rows of a plain product, at most 5 a holder on
+// average.  Microseconds for it and for the tcgen05 form with tiles of 64 rows:
+//   plain, MXFP4, N x K of W:  M = 3   11008 x 2048: 9.5 / 12.2, 28672 x 4096: 25 / 36
+//                              M = 8   11008 x 2048: 10.4 / 12.2, 28672 x 4096: 27 / 36, 4096 x 4096: 11.5 / 10.8
+//   64 experts of 1408 x 2048: 192 rows 39 / 46 (NVFP4 34 / 40, INT4 43 / 45), 256 rows 39 / 46
+//   (tiles of 16 rows, in its time: 512 rows 61 / 46; plain, M = 13, 4096 x 4096: 14.4 / 10.9)
+template <int FMT>
+bool expert_gemv_serves(const wq::ExpertArgs& a) {
+  const int64_t holders = std::min(a.E, a.T);
+  return (a.E == 1 ? a.T <= wq::kVecRows : a.T <= 5 * holders) && expert_gemv_split<FMT>(a.K) > 0;
 }
 
 // The CUDA-core form, one row of X at a time (MT = 2: the two rows of a plain product).
@@ -714,11 +749,11 @@ int launch_expert_rows_mt(const wq::ExpertArgs& a, cudaStream_t st) {
   int ksplit = 1;
   while (ksplit < wq::kRowWarps && ksplit * 2 <= (a.K + 1023) / 1024) ksplit *= 2;
   const int per = wq::kRowRows * wq::kRowWarps / ksplit;
-  constexpr int kSmem = 2 * wq::kRowWarps * wq::kRowRows * 512;
+  constexpr int kSmem = 2 * wq::kRowWarps * wq::kRowRows * 512, kInv = wq::kRowWarps * 4096;
   static std::atomic<uint64_t> attr_done{0};
-  if (int e = ensure_smem_attr(wq::expert_row_kernel<FMT, MT>, kSmem, &attr_done, "expert row smem attribute")) return e;
+  if (int e = ensure_smem_attr(wq::expert_row_kernel<FMT, MT>, kSmem + kInv, &attr_done, "expert row smem attribute")) return e;
   return launch_pdl(wq::expert_row_kernel<FMT, MT>, dim3(unsigned((a.N + per - 1) / per), unsigned(a.T / MT)),
-                    dim3(wq::kRowWarps * 32), kSmem, st, "expert row launch", a, ksplit);
+                    dim3(wq::kRowWarps * 32), a.inv_s ? kSmem + kInv : kSmem, st, "expert row launch", a, ksplit);
 }
 
 template <int FMT>
@@ -732,18 +767,14 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   // each adds at most one partly filled tile
   const int64_t holders = std::min(a.E, a.T);
   const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
-  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, 1, items(192), st);
+  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, false, items(192), st);
   wq::ExpertArgs v = a;
   v.X = X; v.packed = static_cast<const uint8_t*>(packed);
   // rows of X one by one (both rows of a plain product): few enough that no expert is likely
   // to hold several
   if (a.offsets ? a.T <= kExpertRowsMax : a.T <= 2) return launch_expert_rows<FMT>(v, st);
-  bool wide = false;
-  if (expert_gemv_serves<FMT>(a, &wide)) return launch_expert_gemv<FMT>(v, wide, st);
-  const int64_t n = items(64);
-  const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
-  const int split = int(std::max<int64_t>(1, std::min<int64_t>({wq::kTcMaxCtas / n, 8, chunks})));
-  return launch_expert_shape<FMT, wq::ExpNarrow>(a, X, packed, split, n, st);
+  if (expert_gemv_serves<FMT>(a)) return launch_expert_gemv<FMT>(v, st);
+  return launch_expert_shape<FMT, wq::ExpNarrow>(a, X, packed, true, items(64), st);
 }
 
 int launch_experts(const wq::ExpertArgs& a, int fmt, const uint16_t* X, const void* packed, cudaStream_t st) {
