@@ -597,8 +597,9 @@ def wq_linear_mxfp4(X: torch.Tensor, p: PackedMXFP4, act_fp4: int = 0, act_inv_s
     Y = X.new_empty((M, p.N)) if out is None else out
     _dev(Y, "out", torch.bfloat16, (M, p.N))
     s = _opt_f32(act_inv_s, "act_inv_s", K)
-    if ws is None and act_fp4:
-        ws = X.new_empty(linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4), dtype=torch.uint8)
+    if ws is None and (act_fp4 or s is not None):
+        need = linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4)
+        ws = X.new_empty(need, dtype=torch.uint8) if need else None
     _call("wq_linear_mxfp4", _device_of(X, p.codes, p.bscale, Y, s, ws), X.data_ptr(), M, p.N, K, p.codes.data_ptr(),
           p.bscale.data_ptr(), act_fp4, _addr(s), Y.data_ptr(), _addr(ws),
           0 if ws is None else ws.numel() * ws.element_size())

@@ -96,6 +96,28 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_pack_kernel(const uint16_t* 
   }
 }
 
+// X 1/s in bf16, for the W4A16 product: one rounding of 2^-9 a term, as the product would
+// otherwise round the weight times 1/s, but once an element of X instead of once for every
+// weight in every row tile.
+__global__ void __launch_bounds__(kMxThreads) mxfp4_scale_kernel(const uint16_t* __restrict__ X,
+                                                                 const float* __restrict__ s, uint64_t words,
+                                                                 uint32_t row_words, uint16_t* __restrict__ out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (uint64_t u = uint64_t(blockIdx.x) * kMxThreads + threadIdx.x; u < words; u += uint64_t(gridDim.x) * kMxThreads) {
+    const uint4 raw = ldg_v4(X + u * 8);
+    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+    const float4* f = reinterpret_cast<const float4*>(s) + 2 * (u % row_words);
+    const float4 f0 = __ldg(f), f1 = __ldg(f + 1);
+    const float fv[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pack_bf16x2(__uint_as_float(r[j] << 16) * fv[2 * j], __uint_as_float(r[j] & 0xFFFF0000u) * fv[2 * j + 1]);
+    reinterpret_cast<uint4*>(out)[u] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 // The values of a pack in bf16: exact (at most two significant bits, exponents -128 .. 129; a
 // scale byte of 254, which the pack never writes, may overflow to infinity).
 __global__ void __launch_bounds__(kMxThreads) mxfp4_unpack_kernel(const uint32_t* __restrict__ codes,
