@@ -15,7 +15,7 @@
 //
 // One CTA walks items (expert, row tile, 128 weight rows).  Roles:
 //   warp 0       codes [128 x 256 k] by TMA into a ring of WS stages
-//   warp 1       X boxes [XBOX rows x 64 k] by TMA into a ring of XS slots of SK
+//   warp 1       X boxes [rows x 64 k] by TMA into a ring of XS slots of SK
 //                k-blocks (64 k) each
 //   warp 2       TMEM allocation and the MMA issuer (a whole warp in step, one
 //                elected lane issues: a lone lane's branch costs 46 clocks an
@@ -43,7 +43,7 @@ constexpr int kExpChunk = 256;     // k per stage of codes (128 bytes a row)
 
 struct ExpertArgs {
   CUtensorMap tmW;         // codes u8 [E * N, K / 2], box {128, 128}, 128B swizzle
-  CUtensorMap tmX;         // X bf16 [T, K], box {64, XBOX}, 128B swizzle
+  CUtensorMap tmX[6];      // X bf16 [T, K], boxes {64, xunit * (1 .. xmaps)}, 128B swizzle
   const uint16_t* X;       // bf16 [T, K]
   const uint8_t* packed;   // K / 2 bytes per row, rows [E * N]
   const int* offsets;      // [E + 1], or null: one expert over all T rows
@@ -55,6 +55,7 @@ struct ExpertArgs {
   uint16_t* Y;             // bf16 [T, N]
   int E, N, K, T;
   int log2g;
+  int xunit, xmaps;        // heights of X's boxes
   int split;               // CTAs of a cluster that share an item along K (1: none)
 };
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile
   return lo;
 }
 
-// Up to XT rows of X per item, in boxes of XBOX; NACC accumulators (2: the
+// Up to XT rows of X per item; NACC accumulators (2: the
 // epilogue overlaps the next item); WS stages of codes.  X slots and stages of
 // dequantized weights hold SK k-blocks each: one pair of waits and one commit of the
 // MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.
@@ -116,9 +117,13 @@ __device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile
 // Scales are fetched for many chunks at once, SEG bytes a row, because a warp's copy
 // of 4 bytes from each of 32 rows takes as long as one of 16 bytes (about 200 clocks,
 // more than the chunk's products).
-template <int XT_, int XBOX_, int NACC_, int WS_, int XS_, int SK_, int SEG_>
+//
+// A k-block of X is one TMA box of the item's height, rounded up to XUNIT (a map for each):
+// a box takes its thread about 100 clocks whatever its height, and six of 32 rows took
+// longer than the k-block's products.
+template <int XT_, int XUNIT_, int NACC_, int WS_, int XS_, int SK_, int SEG_>
 struct ExpShape {
-  static constexpr int XT = XT_, XBOX = XBOX_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_, SEG = SEG_;
+  static constexpr int XT = XT_, XUNIT = XUNIT_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_, SEG = SEG_;
   static constexpr int AS = SK == 1 ? 4 : 2;  // stages of dequantized weights, 32 SK columns each
   static constexpr int CODE_BYTES = 128 * 128;
   static constexpr int SC_PITCH = SEG + 16;     // a row's scales of a segment (a word more where rows start inside one)
@@ -136,13 +141,13 @@ struct ExpShape {
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static_assert(USED_COLS <= 512, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
-  static_assert(XT % 16 == 0 && XT <= 256 && XT % XBOX == 0 && XBOX % 8 == 0, "row tiles");
+  static_assert(XT % 16 == 0 && XT <= 256 && XT % XUNIT == 0 && XUNIT % 16 == 0 && XT / XUNIT <= 6, "row tiles");
   static_assert(SEG == 32 || SEG == 64, "a chunk takes 4 to 16 bytes of scales");
   static_assert(4 % SK == 0 && XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
 using ExpWide = ExpShape<192, 32, 2, 3, 3, 2, 32>;
-using ExpNarrow = ExpShape<64, 8, 2, 5, 3, 4, 64>;
+using ExpNarrow = ExpShape<64, 16, 2, 5, 3, 4, 64>;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     if (lane == 0) {
       *abort_flag = 0;
       prefetch_tmap(&a.tmW);
-      prefetch_tmap(&a.tmX);
+      for (int b = 0; b < a.xmaps; ++b) prefetch_tmap(&a.tmX[b]);
     }
   } else if (warp == 2) {
     tmem_alloc(tmem_slot, S::TMEM_COLS);
@@ -458,19 +463,18 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     bool ok = true;
     for (int id = first; id < items && ok; id += step) {
       const Item it = item_of(id);
-      const int boxes = (it.rows + S::XBOX - 1) / S::XBOX;
+      const int box = min((it.rows + a.xunit - 1) / a.xunit, a.xmaps);
       for (int c = c0; c < c1 && ok; ++c) {
         const int nst = stages_of(c);
         for (int h = 0; h < nst; ++h, ++q) {
           if (q >= XS) ok = warp_wait(&mdone[s], par, ERR_TIMEOUT_PIPE, abort_flag);
           if (!ok) break;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&xfull[s], uint32_t(SK * boxes * S::XBOX) * 128u);
+            mbar_arrive_expect_tx(&xfull[s], uint32_t(SK * box * a.xunit) * 128u);
 #pragma unroll
             for (int j = 0; j < SK; ++j)
-              for (int b = 0; b < boxes; ++b)
-                tma_load_2d(smem + S::OFF_X + s * S::SLOT_BYTES + j * XT * 128 + b * S::XBOX * 128, &a.tmX, &xfull[s],
-                            c * kExpChunk + (h * SK + j) * 64, it.row + b * S::XBOX);
+              tma_load_2d(smem + S::OFF_X + s * S::SLOT_BYTES + j * XT * 128, &a.tmX[box - 1], &xfull[s],
+                          c * kExpChunk + (h * SK + j) * 64, it.row);
           }
           __syncwarp();
           if (++s == XS) {
@@ -556,6 +560,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
       const Item it = item_of(id);
       // row of the weights (mod 2^32: only its bytes' place within a word is asked for)
       const uint32_t srow = uint32_t(it.e) * uint32_t(a.N) + uint32_t(min(it.n0 + trow, a.N - 1));
+      const bool past = it.n0 + trow >= a.N;
       for (int c = c0, cs = c0 % cps; c < c1; ++c) {  // cs: chunk within its segment
         const int nst = stages_of(c);
         if (c == c0 || cs == 0) ok = warp_wait(&sfull[sg & 1], (sg >> 1) & 1, ERR_TIMEOUT_PIPE, abort_flag);
@@ -604,8 +609,9 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t e8 = (sc >> (8 * h)) & 255u;
-              // a scale that is a normal fp16 (2^-14 .. 2^15) for the whole warp, or fp32 products
+              // a scale that is a normal fp16 (2^-14 .. 2^15) for the whole warp, or fp32 products; rows
+              // past N count for none (their sums are not used)
+              const uint32_t e8 = past ? 127u : (sc >> (8 * h)) & 255u;
               if (!a.inv_s && __all_sync(0xffffffffu, e8 - 113u < 30u)) {
                 const uint32_t s2 = (e8 - 112u) << 10;
 #pragma unroll

@@ -649,9 +649,14 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
   if (int e = make_tmap_2d(&a.tmW, packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.E) * uint64_t(a.N),
                            uint64_t(a.K / 2), 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
-  if (int e = make_tmap_2d(&a.tmX, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(a.T), uint64_t(a.K), S::XBOX, 64,
-                           CU_TENSOR_MAP_SWIZZLE_128B))
-    return e;
+  // heights of X's boxes: those of the plain product's even tiles, or every multiple of XUNIT
+  const int64_t xtiles = (a.T + S::XT - 1) / S::XT;
+  a.xunit = a.offsets ? S::XUNIT : int((a.T + xtiles - 1) / xtiles + 15) & ~15;
+  a.xmaps = a.offsets ? S::XT / S::XUNIT : 1;
+  for (int b = 0; b < a.xmaps; ++b)
+    if (int e = make_tmap_2d(&a.tmX[b], X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, uint64_t(a.T), uint64_t(a.K),
+                             uint32_t(a.xunit * (b + 1)), 64, CU_TENSOR_MAP_SWIZZLE_128B))
+      return e;
   static std::atomic<uint64_t> attr_done{0};
   if (int e = ensure_smem_attr(wq::expert_gemm_kernel<FMT, S>, S::SMEM_BYTES, &attr_done, "expert smem attribute"))
     return e;
