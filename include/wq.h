@@ -96,10 +96,10 @@ int wq_mxfp4_sizes(int64_t N, int64_t K, size_t* codes_bytes, size_t* bscale_byt
 /* Scratch bytes wq_linear_int4 / wq_linear_nvfp4 / wq_linear_mxfp4 use for an
  * [M, K] x [N, K] problem (format WQ_FMT_*, act_fp4 as in wq_linear_nvfp4).
  * W4A4 requires a workspace of this size.  W4A16 never requires one.  For
- * MXFP4 a non-zero size (M > 8) is room for X * act_inv_s: given it, a call
- * with act_inv_s scales X once instead of the weights for every 64 to 192
- * rows (a call without act_inv_s does not use it).  For INT4 and NVFP4 it
- * means a
+ * MXFP4 a non-zero size (M > 8, or M > 2 and K > 6656) is room for
+ * X * act_inv_s: given it, a call with act_inv_s scales X once instead of the
+ * weights for every 192 rows (a call without act_inv_s does not use it).
+ * For INT4 and NVFP4 it means a
  * prefill GEMM with few output tiles (under half the SMs) that, given a
  * workspace of at least this size, splits K over several CTAs per tile (fp32
  * partial tiles, then a reduction launch that sums them in split order, so the
@@ -334,9 +334,11 @@ int wq_linear_nvfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
 /* wq_linear_mxfp4 -- Y = (X * act_inv_s) * dequant(Wq)^T for an MXFP4 pack.
  *   act_fp4 = 0: W4A16, activations stay bf16.  With act_inv_s each term is
  *            rounded to bf16 once, as X * act_inv_s (given the workspace of
- *            wq_linear_workspace_size; M > 8) or as the weight times
- *            act_inv_s (without; M <= 8 holds the product to 2^-11 or
- *            better).
+ *            wq_linear_workspace_size) or as the weight times act_inv_s
+ *            (without).  Sizes that ask for no workspace hold
+ *            X * act_inv_s to 2^-11 instead, as fp16 scaled by a power of
+ *            two per row (of a run of 32 k for M <= 2): below 2^-39 of the
+ *            row's (run's) largest finite magnitude it counts as zero.
  *   act_fp4 = 1: W4A4: X * act_inv_s is first quantized to MXFP4 along K (the
  *            wq_quantize_mxfp4 rule applied to X), and the product runs on the
  *            block-scaled FP4 tensor cores; K % 64 == 0; needs workspace.
@@ -367,7 +369,9 @@ typedef struct {
  *            no copy of it), 4-byte aligned, not decreasing, within [0, T]
  *   Y        bf16 [T, N]; rows before offsets[0] and from offsets[E] on are
  *            left as they were
- * W4A16, fp32 accumulation, no workspace.  An expert may hold no row or all of
+ * W4A16, fp32 accumulation, no workspace.  Up to 5 rows an expert, X may be held
+ * as fp16 scaled by a power of two per row: exact down to 2^-31 of the row's
+ * largest finite magnitude, to 2^-39 of it below.  An expert may hold no row or all of
  * them; T = 0 computes nothing (X, Y and offsets may then be NULL).  Offsets
  * that decrease or leave [0, T] make the call compute nothing, and the next
  * wq_device_error returns WQ_ERR_ARG. */

@@ -109,10 +109,12 @@ __device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile
   return lo;
 }
 
-// Up to XT rows of X per item; NACC accumulators (2: the
+// Shape of the tcgen05 form: up to XT rows of X per item; NACC accumulators (2: the
 // epilogue overlaps the next item); WS stages of codes.  X slots and stages of
 // dequantized weights hold SK k-blocks each: one pair of waits and one commit of the
-// MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.
+// MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.  The same
+// shape serves few rows: an item's boxes and MMAs are as high as its rows (tiles of 64 rows
+// with deeper stages were within 2% at 13 to 1000 rows, and slower from 64 an expert on).
 //
 // Scales are fetched for many chunks at once, SEG bytes a row, because a warp's copy
 // of 4 bytes from each of 32 rows takes as long as one of 16 bytes (about 200 clocks,
@@ -120,11 +122,10 @@ __device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile
 //
 // A k-block of X is one TMA box of the item's height, rounded up to XUNIT (a map for each):
 // a box takes its thread about 100 clocks whatever its height, and six of 32 rows took
-// longer than the k-block's products.
-template <int XT_, int XUNIT_, int NACC_, int WS_, int XS_, int SK_, int SEG_>
+// longer than the k-block's products (2048 x 11008 x 2048: 76.7 -> 73.4 us).
 struct ExpShape {
-  static constexpr int XT = XT_, XUNIT = XUNIT_, NACC = NACC_, WS = WS_, XS = XS_, SK = SK_, SEG = SEG_;
-  static constexpr int AS = SK == 1 ? 4 : 2;  // stages of dequantized weights, 32 SK columns each
+  static constexpr int XT = 192, XUNIT = 32, NACC = 2, WS = 3, XS = 3, SK = 2, SEG = 32;
+  static constexpr int AS = 2;                  // stages of dequantized weights, 32 SK columns each
   static constexpr int CODE_BYTES = 128 * 128;
   static constexpr int SC_PITCH = SEG + 16;     // a row's scales of a segment (a word more where rows start inside one)
   static constexpr int Z_PITCH = SEG / 4 + 4;   // a row's zero points of a segment: SEG / 2 groups
@@ -136,18 +137,14 @@ struct ExpShape {
   static constexpr int OFF_BAR = OFF_TAB + 2 * (kMaxExperts + 4) * 4;
   static constexpr int NBAR = 2 * WS + 2 * XS + AS + 2 * NACC + 4;
   static constexpr int SMEM_BYTES = OFF_BAR + NBAR * 8 + 64 + 1024;
-  static constexpr int A_COL = NACC * XT;
-  static constexpr int USED_COLS = A_COL + AS * SK * 32;
-  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
-  static_assert(USED_COLS <= 512, "tensor memory columns");
+  static constexpr int A_COL = NACC * XT;       // tensor memory: accumulators, then dequantized weights
+  static constexpr int TMEM_COLS = 512;
+  static_assert(A_COL + AS * SK * 32 <= TMEM_COLS, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
-  static_assert(XT % 16 == 0 && XT <= 256 && XT % XUNIT == 0 && XUNIT % 16 == 0 && XT / XUNIT <= 6, "row tiles");
-  static_assert(SEG == 32 || SEG == 64, "a chunk takes 4 to 16 bytes of scales");
-  static_assert(4 % SK == 0 && XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
+  static_assert(XT % XUNIT == 0 && XUNIT % 16 == 0, "row tiles");
+  static_assert(XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
-using ExpWide = ExpShape<192, 32, 2, 3, 3, 2, 32>;
-using ExpNarrow = ExpShape<64, 16, 2, 5, 3, 4, 64>;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -281,8 +278,9 @@ __device__ __forceinline__ void dequant8_e2m1_f32(uint32_t w, float s, const flo
   for (int i = 0; i < 4; ++i) out[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
 }
 
-template <int FMT, typename S>
+template <int FMT>
 __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertArgs a) {
+  using S = ExpShape;
   constexpr int XT = S::XT, WS = S::WS, XS = S::XS, NACC = S::NACC, SK = S::SK, AS = S::AS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -733,12 +731,10 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 // is why both operands are fp16: a pair of E2M1 codes is one conversion and one product
 // there, against one conversion, two multiply-adds and a packing in bf16.
 //
-// A unit is 16 weight rows of one row tile; a step of it is 128 k.  A cluster of
-// `split` CTAs takes a contiguous share of the units, each of its CTAs a share of K (so
-// that a tile's rows fit shared memory), each of a CTA's 16 warps a contiguous share of
-// the CTA's steps: every SM streams the same number of bytes whatever N and K are.
-// Units that straddle warps are summed through shared memory, in warp order, and
-// the CTAs of a cluster through distributed shared memory, in rank order.
+// A unit is 16 weight rows of one row tile; a step of it is 128 k.  A CTA takes a
+// contiguous share of the units, each of its 16 warps a contiguous share of the CTA's
+// steps: every SM streams the same number of bytes whatever N and K are.  Units that
+// straddle warps are summed through shared memory, in warp order.
 //
 // X is staged once per row tile in the order of the MMA's B fragments, each row scaled
 // by a power of two that puts its largest finite magnitude at 2^14: fp16 then holds
@@ -763,18 +759,15 @@ constexpr int kVecDepth = 6;
 constexpr int kVecRows = 8;  // rows of X of a tile
 constexpr int kVecRing = kVecWarps * kVecDepth * 1024;
 
-// Shared memory: codes [warp][kVecDepth][2][32 lanes][16 bytes], the CTA's sums of a run of units
-// (where a cluster shares them), sums of units that straddle warps, X fragments.
+// Shared memory: codes [warp][kVecDepth][2][32 lanes][16 bytes], sums of units that straddle
+// warps, X fragments (all of K: MAX_STEPS is what this form serves).
 template <int FMT>
 struct VecShape {
-  static constexpr int SUM_BYTES = 16 * 8 * 4;                   // one unit's sums
-  static constexpr int MAX_UNITS = 16;
-  static constexpr int OFF_SUMS = kVecRing;
-  static constexpr int OFF_PART = OFF_SUMS + MAX_UNITS * SUM_BYTES;
-  static constexpr int OFF_X = OFF_PART + 2 * kVecWarps * SUM_BYTES;
-  static constexpr int FRAG_BYTES = 2048;                        // X fragments of a step
+  static constexpr int OFF_PART = kVecRing;
+  static constexpr int OFF_X = OFF_PART + 2 * kVecWarps * 16 * kVecRows * 4;
+  static constexpr int FRAG_BYTES = 2048;                                        // X fragments of a step
   static constexpr int STEP_BYTES = FRAG_BYTES + (FMT == GEMM_INT4 ? 256 : 0);  // and P, Q of its groups
-  static constexpr int MAX_STEPS = (216 * 1024 - OFF_X) / STEP_BYTES;
+  static constexpr int MAX_STEPS = (216 * 1024 - OFF_X) / STEP_BYTES;           // 52, INT4 46
 };
 
 __device__ __forceinline__ uint32_t ldg_u16(const void* p) { return __ldg(static_cast<const uint16_t*>(p)); }
@@ -797,7 +790,6 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   __shared__ uint32_t rtop[kVecRows];                     // largest finite magnitude of X's rows, fp32 bits
   __shared__ float rscale[kVecRows];                      // what undoes their scaling
   float (*part)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_PART);
-  float (*sums)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_SUMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int K = a.K, N = a.N;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -809,19 +801,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   }
   const int tiles = a.offsets ? tstart[a.E] : (a.T + kVecRows - 1) / kVecRows;
   const int nrb = (N + 15) >> 4;                        // row blocks of an expert
-  // this cluster's units, this CTA's steps of each
-  int rank = 0, cl = blockIdx.x, ncl = gridDim.x, S0 = 0, S = (K + 127) >> 7;
-  if (a.split > 1) {
-    rank = int(cluster_ctarank());
-    cl /= a.split;
-    ncl /= a.split;
-    const int all = S;
-    S0 = all * rank / a.split;
-    S = all * (rank + 1) / a.split - S0;
-  }
-  const int units = tiles * nrb, per = units / ncl, more = units - per * ncl;
-  int u0 = cl * per + min(cl, more);
-  const int ulast = u0 + per + (cl < more);
+  const int S = (K + 127) >> 7;                         // steps of a unit
+  const int units = tiles * nrb, per = units / int(gridDim.x), more = units - per * int(gridDim.x);
+  int u0 = int(blockIdx.x) * per + min(int(blockIdx.x), more);
+  const int ulast = u0 + per + (int(blockIdx.x) < more);
 
   const int zw = (((FMT == GEMM_INT4 ? K / G : 8) + 7) >> 3) * 4;  // zero-point bytes of a row
   const int sw = FMT == GEMM_INT4 ? K / G * 2 : FMT == GEMM_NVFP4 ? K >> 4 : K >> 5;  // scale bytes of a row
@@ -834,8 +817,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   while (u0 < ulast) {
     // ---- a run of units of one row tile
     const int tile = u0 / nrb;
-    int u1 = min(ulast, (tile + 1) * nrb);
-    if (a.split > 1) u1 = min(u1, u0 + V::MAX_UNITS);
+    const int u1 = min(ulast, (tile + 1) * nrb);
     int e = 0, row = tile * kVecRows, rows = min(kVecRows, a.T - row);
     if (a.offsets) {
       e = expert_of_tile(tstart, a.E, tile);
@@ -857,12 +839,12 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     uint32_t put = ring;
     const auto open_codes = [&]() {
       const int64_t rlo = row_of(cu, g), rhi = row_of(cu, g + 8);
-      plo = a.packed + rlo * (K >> 1) + (S0 + cj) * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
+      plo = a.packed + rlo * (K >> 1) + cj * 64 + (FMT == GEMM_INT4 ? c * (G / 8) : 16 * c);
       phi = plo + (rhi - rlo) * (K >> 1);
     };
     const auto open_scales = [&]() {
       const int64_t rlo = row_of(su, g), d = row_of(su, g + 8) - rlo;
-      slo = scales + rlo * sw + (S0 + sj) * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
+      slo = scales + rlo * sw + sj * SB + (FMT == GEMM_NVFP4 ? 2 * c : FMT == GEMM_MXFP4 ? c : 0);
       shi = slo + d * sw;
       zlo = reinterpret_cast<const uint8_t*>(a.zeros) + rlo * zw;
       zhi = zlo + d * zw;
@@ -871,7 +853,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     const auto request = [&]() {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const int k0 = (S0 + cj) * 128;
+        const int k0 = cj * 128;
         const bool in = FULL || (FMT == GEMM_INT4 ? k0 + i * G < K : k0 + 32 * c < K);
         cp_async_zfill<16 / NG>(put + i * (16 / NG), in ? plo + i * (G / 2) : a.packed, in ? 16 / NG : 0);
         cp_async_zfill<16 / NG>(put + 512 + i * (16 / NG), in ? phi + i * (G / 2) : a.packed, in ? 16 / NG : 0);
@@ -901,7 +883,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       } else {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          const bool in = FULL || (FMT == GEMM_INT4 ? ((S0 + sj) * NG + i) * 2 < sw : (S0 + sj) * 128 + 32 * c < K);
+          const bool in = FULL || (FMT == GEMM_INT4 ? (sj * NG + i) * 2 < sw : sj * 128 + 32 * c < K);
           r.l[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(slo) : ldg_u16(slo + 2 * i);
           r.h[i] = !in ? 0u : FMT == GEMM_MXFP4 ? ldg_u8(shi) : ldg_u16(shi + 2 * i);
         }
@@ -910,7 +892,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       shi += SB;
       r.zl = r.zh = 0x8888u;
       if (FMT == GEMM_INT4 && a.zeros) {
-        const int b = ((S0 + sj) * NG) >> 1;
+        const int b = (sj * NG) >> 1;
         r.zl = G == 32 ? ldg_u16(zlo + b) : ldg_u8(zlo + b);
         r.zh = G == 32 ? ldg_u16(zhi + b) : ldg_u8(zhi + b);
       }
@@ -944,12 +926,11 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       // X, or X * act_inv_s, 256 k of a row at a time: the rows' largest finite magnitudes, then the fragments
       if (threadIdx.x < kVecRows) rtop[threadIdx.x] = 0;
       __syncthreads();  // also: the last run's readers are done
-      const float* f = FMT == GEMM_MXFP4 && a.inv_s ? a.inv_s + S0 * 128 : nullptr;
-      const int len = min(S * 128, K - S0 * 128);
+      const float* f = FMT == GEMM_MXFP4 ? a.inv_s : nullptr;
       // each row by two warps, alternate runs of 256 k
       constexpr int WPR = kVecWarps / kVecRows;
       const int m = warp / WPR, kend = m < rows ? S * 128 : 0;
-      const uint16_t* xrow = a.X + int64_t(row + min(m, rows - 1)) * K + S0 * 128;
+      const uint16_t* xrow = a.X + int64_t(row + min(m, rows - 1)) * K;
       // four runs' loads in flight at once, twice over (the second time from L1)
       const auto pass = [&](auto&& use) {
 #pragma unroll 1
@@ -959,10 +940,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int k = kk + q * WPR * 256;
-            r[q] = k < len ? ldg_v4(xrow + k) : make_uint4(0, 0, 0, 0);
+            r[q] = k < K ? ldg_v4(xrow + k) : make_uint4(0, 0, 0, 0);
             if (FMT == GEMM_MXFP4) {
               f0[q] = f1[q] = make_float4(1.f, 1.f, 1.f, 1.f);
-              if (f && k < len) {
+              if (f && k < K) {
                 f0[q] = __ldg(reinterpret_cast<const float4*>(f + k));
                 f1[q] = __ldg(reinterpret_cast<const float4*>(f + k) + 1);
               }
@@ -1056,7 +1037,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           mma_f16_16816(d, a0, a1, a2, a3, x.x, x.y);
           mma_f16_16816(d, b0, b1, b2, b3, x.z, x.w);
           if (w % WPG == WPG - 1) {
-            const int gi = w / WPG, nib = 4 * ((G == 128 ? ((S0 + j) & 1) : 0) + gi);
+            const int gi = w / WPG, nib = 4 * ((G == 128 ? (j & 1) : 0) + gi);
             const bool words = FULL && NG > 1;
             const uint32_t s2 = prmt_b32(r.l[words ? gi & ~1 : gi], r.h[words ? gi & ~1 : gi],
                                          words && (gi & 1) ? 0x7632 : 0x5410);
@@ -1166,8 +1147,6 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
         // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
         if (!whole) {
           part[2 * warp + begun][r][m] = y;
-        } else if (a.split > 1) {
-          sums[u][r][m] = y;
         } else if (m < rows && nb0 + u * 16 + r < N) {
           a.Y[int64_t(row + m) * N + nb0 + u * 16 + r] = uint16_t(pack_bf16x2(y, y));
         }
@@ -1194,27 +1173,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = (lane + 32 * q) >> 3, m = lane & 7;
-        if (a.split > 1) {
-          sums[us][r][m] = y[q];
-        } else if (m < rows && nb0 + us * 16 + r < N) {
+        if (m < rows && nb0 + us * 16 + r < N) {
           a.Y[int64_t(row + m) * N + nb0 + us * 16 + r] = uint16_t(pack_bf16x2(y[q], y[q]));
         }
       }
-    }
-    if (a.split > 1) {
-      cluster_sync();  // every CTA of the cluster has its sums in shared memory
-      for (int i = rank * int(blockDim.x) + threadIdx.x; i < (u1 - u0) * 128; i += a.split * int(blockDim.x)) {
-        const int r = i & 15, m = (i >> 4) & 7, uu = i >> 7;
-        if (m >= rows || nb0 + uu * 16 + r >= N) continue;
-        const uint32_t at_sum = smem_u32(&sums[uu][r][m]);
-        float v[8], y = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < a.split ? ld_shared_cluster_f32(map_shared_rank(at_sum, uint32_t(k))) : 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y += v[k];
-        a.Y[int64_t(row + m) * N + nb0 + uu * 16 + r] = uint16_t(pack_bf16x2(y, y));
-      }
-      cluster_sync();  // the sums stay until every rank has read them
     }
     u0 = u1;
   }

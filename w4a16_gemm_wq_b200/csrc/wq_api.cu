@@ -643,9 +643,16 @@ int resident_clusters(Kern kern, int threads, size_t smem, int split, std::atomi
   return n;
 }
 
-template <int FMT, typename S>
-int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed, bool splits, int64_t items,
-                        cudaStream_t st) {
+// (expert, row tile, 128 weight rows) at most: the host does not know how the rows fall on the
+// experts, at most min(E, T) hold any, and each adds at most one partly filled tile.
+int64_t expert_items(const wq::ExpertArgs& a) {
+  return (std::min(a.E, a.T) + a.T / wq::ExpShape::XT) * ((int64_t(a.N) + 127) / 128);
+}
+
+template <int FMT>
+int launch_expert_gemm(wq::ExpertArgs a, const uint16_t* X, const void* packed, cudaStream_t st) {
+  using S = wq::ExpShape;
+  const int64_t items = expert_items(a);
   if (int e = make_tmap_2d(&a.tmW, packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(a.E) * uint64_t(a.N),
                            uint64_t(a.K / 2), 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return e;
@@ -658,17 +665,17 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
                              uint32_t(a.xunit * (b + 1)), 64, CU_TENSOR_MAP_SWIZZLE_128B))
       return e;
   static std::atomic<uint64_t> attr_done{0};
-  if (int e = ensure_smem_attr(wq::expert_gemm_kernel<FMT, S>, S::SMEM_BYTES, &attr_done, "expert smem attribute"))
+  if (int e = ensure_smem_attr(wq::expert_gemm_kernel<FMT>, S::SMEM_BYTES, &attr_done, "expert smem attribute"))
     return e;
   // few items: K shared by a cluster.  The split that ends first, counting a launch's start and
   // end as three chunks of K and the sum over the cluster as one
   const int64_t chunks = (a.K + wq::kExpChunk - 1) / wq::kExpChunk;
   a.split = 1;
-  if (splits && items < wq::kTcMaxCtas) {
+  if (items < wq::kTcMaxCtas) {
     static std::atomic<uint64_t> seen[kExpMaxSplit + 1];
     int64_t best = chunks + 3;
     for (int sp = 2; sp <= std::min<int64_t>(kExpMaxSplit, chunks); ++sp) {
-      const int64_t at_once = resident_clusters(wq::expert_gemm_kernel<FMT, S>, wq::kExpThreads, S::SMEM_BYTES, sp, seen);
+      const int64_t at_once = resident_clusters(wq::expert_gemm_kernel<FMT>, wq::kExpThreads, S::SMEM_BYTES, sp, seen);
       const int64_t t = (items + at_once - 1) / at_once * ((chunks + sp - 1) / sp + 4);
       if (t < best) {
         best = t;
@@ -678,45 +685,26 @@ int launch_expert_shape(wq::ExpertArgs a, const uint16_t* X, const void* packed,
   }
   ClusterLaunch l(wq::kExpThreads, S::SMEM_BYTES, a.split, st);
   l.cfg.gridDim.x = unsigned(a.split > 1 ? items * a.split : std::min<int64_t>(items, wq::kTcMaxCtas));
-  return cuda_check(cudaLaunchKernelEx(&l.cfg, wq::expert_gemm_kernel<FMT, S>, a), "expert gemm launch");
+  return cuda_check(cudaLaunchKernelEx(&l.cfg, wq::expert_gemm_kernel<FMT>, a), "expert gemm launch");
 }
 
-// The mma.sync form for few rows per expert.  The fewest CTAs of a cluster that share K for a
-// tile's rows to fit their shared memory (0: more than a portable cluster).
+// The mma.sync form for few rows per expert serves a K whose staged rows fit shared memory.
 template <int FMT>
-int expert_gemv_split(int64_t K) {
-  const int64_t steps = (K + 127) / 128, most = wq::VecShape<FMT>::MAX_STEPS, sp = (steps + most - 1) / most;
-  return sp <= kExpMaxSplit ? int(sp) : 0;
+bool expert_gemv_serves(int64_t K) {
+  return (K + 127) / 128 <= wq::VecShape<FMT>::MAX_STEPS;
 }
 
 template <int FMT, int G, bool FULL>
-int launch_expert_gemv_full(wq::ExpertArgs a, cudaStream_t st) {
+int launch_expert_gemv_full(const wq::ExpertArgs& a, cudaStream_t st) {
   using V = wq::VecShape<FMT>;
-  const int64_t holders = std::min(a.E, a.T);
-  const int64_t units = (holders + a.T / wq::kVecRows) * ((int64_t(a.N) + 15) / 16);
+  const int64_t units = (std::min(a.E, a.T) + a.T / wq::kVecRows) * ((int64_t(a.N) + 15) / 16);
   static std::atomic<uint64_t> attr_done{0};
   if (int e = ensure_smem_attr(wq::expert_gemv_kernel<FMT, G, FULL>, V::OFF_X + V::MAX_STEPS * V::STEP_BYTES,
                                &attr_done, "expert gemv smem attribute"))
     return e;
-  // of the splits that fit, the one whose busiest CTA has the fewest steps
-  const int64_t steps = (a.K + 127) / 128;
-  const auto smem_of = [&](int sp) { return size_t(V::OFF_X + (steps + sp - 1) / sp * V::STEP_BYTES); };
-  const auto kern = wq::expert_gemv_kernel<FMT, G, FULL>;
-  static std::atomic<uint64_t> seen[kExpMaxSplit + 1];
-  int64_t best = INT64_MAX, clusters = 1;
-  const int least = expert_gemv_split<FMT>(a.K);
-  for (int sp = least; sp <= (least > 1 ? kExpMaxSplit : 1); ++sp) {
-    const int64_t n = std::min<int64_t>(units, resident_clusters(kern, wq::kVecWarps * 32, smem_of(sp), sp, seen));
-    const int64_t t = (units + n - 1) / n * ((steps + sp - 1) / sp);
-    if (t < best) {
-      best = t;
-      a.split = sp;
-      clusters = n;
-    }
-  }
-  ClusterLaunch l(wq::kVecWarps * 32, smem_of(a.split), a.split, st);
-  l.cfg.gridDim.x = unsigned(clusters * a.split);
-  return cuda_check(cudaLaunchKernelEx(&l.cfg, kern, a), "expert gemv launch");
+  return launch_pdl(wq::expert_gemv_kernel<FMT, G, FULL>, dim3(unsigned(std::min<int64_t>(units, wq::kTcMaxCtas))),
+                    dim3(wq::kVecWarps * 32), size_t(V::OFF_X + (a.K + 127) / 128 * V::STEP_BYTES), st,
+                    "expert gemv launch", a);
 }
 
 template <int FMT, int G>
@@ -734,20 +722,7 @@ int launch_expert_gemv(const wq::ExpertArgs& a, cudaStream_t st) {
     return launch_expert_gemv_g<FMT, 0>(a, st);
 }
 
-// Whether that form serves a call: at most 8 rows of a plain product, at most 5 a holder on
-// average.  Microseconds for it and for the tcgen05 form with tiles of 64 rows:
-//   plain, MXFP4, N x K of W:  M = 3   11008 x 2048: 9.5 / 12.2, 28672 x 4096: 25 / 36
-//                              M = 8   11008 x 2048: 10.4 / 12.2, 28672 x 4096: 27 / 36, 4096 x 4096: 11.5 / 10.8
-//   64 experts of 1408 x 2048: 192 rows 39 / 46 (NVFP4 34 / 40, INT4 43 / 45), 256 rows 39 / 46
-//   (tiles of 16 rows, in its time: 512 rows 61 / 46; plain, M = 13, 4096 x 4096: 14.4 / 10.9)
-template <int FMT>
-bool expert_gemv_serves(const wq::ExpertArgs& a) {
-  const int64_t holders = std::min(a.E, a.T);
-  return (a.E == 1 ? a.T <= wq::kVecRows : a.T <= 5 * holders) && expert_gemv_split<FMT>(a.K) > 0;
-}
-
 // The CUDA-core form, one row of X at a time (MT = 2: the two rows of a plain product).
-constexpr int kExpertRowsMax = 16;
 template <int FMT, int MT>
 int launch_expert_rows_mt(const wq::ExpertArgs& a, cudaStream_t st) {
   // warps that share a row block along K: as many as it has runs of 1024 k, a power of two
@@ -766,20 +741,39 @@ int launch_expert_rows(const wq::ExpertArgs& a, cudaStream_t st) {
   return !a.offsets && a.T == 2 ? launch_expert_rows_mt<FMT, 2>(a, st) : launch_expert_rows_mt<FMT, 1>(a, st);
 }
 
+// Which form runs (all three where it says; microseconds, MXFP4 unless it says INT4):
+//   CUDA cores: few rows of which no expert is likely to hold several (up to 16), or the one or
+//     two rows of a plain product while there are few weights to convert for each row (2^25), or
+//     where K is too long for the mma.sync form.
+//       plain, N x K of W            2048 x 2048   11008 x 2048   28672 x 4096   2048 x 11008
+//         1 row   cores / mma.sync    4.7 / 6.4     8.7 / 9.2      28 / 25        11.7 / 14.0
+//         2 rows                      5.1 / 6.4    11.7 / 9.3      40 / 25        10.7 / 14.1
+//       64 experts of 1408 x 2048     8 rows: 9.6 / 16.0, 16: 14.7 / 19.0, 32: 25 / 26
+//   mma.sync: at most 8 rows of a plain product; at most 5 rows a holder, where the tcgen05 form
+//     has more items than one wave.  K up to 6656 (INT4 5888): longer ones, shared by a cluster,
+//     measured slower than the tcgen05 form.
+//       plain, mma.sync / tcgen05     3 rows: 9.4 / 12.2 of 11008 x 2048, 25 / 36 of 28672 x 4096
+//                                     8 rows: 10.2 / 12.3, 27 / 36, and (as a cluster) 16.7 / 14.9 of
+//                                     2051 x 11008; 64 experts of 2048 x 11008, 128 rows: 351 / 292
+//       1408 x 2048, 64 experts       64 rows: 38 / 46 (INT4 44 / 46), 256 rows: 41 / 46 (INT4 46 / 46)
+//                    8 experts        24 rows: 15.6 / 12.8
+//   tcgen05: the rest.
 template <int FMT>
 int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* packed, cudaStream_t st) {
-  // the host does not know how the rows fall on the experts: at most min(E, T) hold any, and
-  // each adds at most one partly filled tile
-  const int64_t holders = std::min(a.E, a.T);
-  const auto items = [&](int xt) { return (holders + a.T / xt) * ((int64_t(a.N) + 127) / 128); };
-  if (a.T / holders > 64) return launch_expert_shape<FMT, wq::ExpWide>(a, X, packed, false, items(192), st);
   wq::ExpertArgs v = a;
   v.X = X; v.packed = static_cast<const uint8_t*>(packed);
-  // rows of X one by one (both rows of a plain product): few enough that no expert is likely
-  // to hold several
-  if (a.offsets ? a.T <= kExpertRowsMax : a.T <= 2) return launch_expert_rows<FMT>(v, st);
-  if (expert_gemv_serves<FMT>(a)) return launch_expert_gemv<FMT>(v, st);
-  return launch_expert_shape<FMT, wq::ExpNarrow>(a, X, packed, true, items(64), st);
+  const bool serves = expert_gemv_serves<FMT>(a.K);
+  if (a.offsets ? a.T <= 16 : a.T <= 2 && (!serves || int64_t(a.T) * a.N * a.K <= 1 << 25))
+    return launch_expert_rows<FMT>(v, st);
+  const bool few = a.E == 1 ? a.T <= wq::kVecRows
+                            : a.T <= 5 * std::min(a.E, a.T) && expert_items(a) > wq::kTcMaxCtas;
+  if (few && serves) return launch_expert_gemv<FMT>(v, st);
+  return launch_expert_gemm<FMT>(a, X, packed, st);
+}
+
+// Whether the MXFP4 Linear of M rows runs on the tcgen05 form, which X 1/s serves better than W 1/s.
+bool mx_scales_x(int64_t M, int64_t K) {
+  return M > wq::kVecRows || (M > 2 && !expert_gemv_serves<wq::GEMM_MXFP4>(K));
 }
 
 int launch_experts(const wq::ExpertArgs& a, int fmt, const uint16_t* X, const void* packed, cudaStream_t st) {
@@ -1186,7 +1180,7 @@ int wq_linear_workspace_size(int64_t M, int64_t N, int64_t K, int format, int ac
   REQUIRE(act_fp4 == 0 || act_fp4 == 1, "act_fp4 must be 0 or 1");
   REQUIRE(!act_fp4 || format != WQ_FMT_INT4, "act_fp4 needs the NVFP4 or the MXFP4 format");
   if (format == WQ_FMT_MXFP4) {
-    *bytes = act_fp4 ? mx_a4_layout(M, K).total : M > wq::kVecRows ? size_t(M) * size_t(K) * 2 : 0;
+    *bytes = act_fp4 ? mx_a4_layout(M, K).total : mx_scales_x(M, K) ? size_t(M) * size_t(K) * 2 : 0;
   } else if (act_fp4) {
     *bytes = w4a4_layout(M, K).total;
   } else {
@@ -1746,9 +1740,9 @@ int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
     f.M = int(M); f.N = int(N); f.K = int(K);
     return launch_mxf4(f, wsb + L.off_codes, codes, st);
   }
-  // More rows than the forms for few take: X 1/s first, where there is room for it (2048 x 11008 x
-  // 2048: 80.6 us against 106, 13 x 2051 x 11008: 19.7 against 21.9); the weights take 1/s otherwise.
-  if (act_inv_s && M > wq::kVecRows && ws && ws_bytes >= size_t(M) * size_t(K) * 2) {
+  // X 1/s first, where there is room for it (2048 x 11008 x 2048: 80.6 us against 106, 13 x 2051 x
+  // 11008: 19.7 against 21.9); the weights take 1/s otherwise.
+  if (act_inv_s && mx_scales_x(M, K) && ws && ws_bytes >= size_t(M) * size_t(K) * 2) {
     REQUIRE_PTR(ws);
     const uint64_t words = uint64_t(M) * uint64_t(K / 8);
     uint16_t* xs = static_cast<uint16_t*>(ws);
