@@ -105,7 +105,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -344,8 +344,8 @@ def _mx_pack(p: PackedMXFP4):
 def wq_dequantize_mxfp4(p: PackedMXFP4, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of an MXFP4 pack, bf16 [N, K] (exact)."""
     _mx_pack(p)
-    W = p.codes.new_empty((p.N, p.K), dtype=torch.bfloat16) if out is None else out
-    _dev(W, "out", torch.bfloat16, (p.N, p.K))
+    W = p.codes.new_empty((p.N, p.K), dtype=torch.bfloat16) if out is None else \
+        _dev(out, "out", torch.bfloat16, (p.N, p.K))
     _call("wq_dequantize_mxfp4", _device_of(p.codes, p.bscale, W), p.codes.data_ptr(), p.bscale.data_ptr(), p.N, p.K,
           W.data_ptr())
     return W
@@ -594,8 +594,7 @@ def wq_linear_mxfp4(X: torch.Tensor, p: PackedMXFP4, act_fp4: int = 0, act_inv_s
     if X.dim() != 2 or X.shape[1] != p.K:
         raise ValueError(f"X must be [M, {p.K}], got {tuple(X.shape)}")
     M, K = X.shape
-    Y = X.new_empty((M, p.N)) if out is None else out
-    _dev(Y, "out", torch.bfloat16, (M, p.N))
+    Y = X.new_empty((M, p.N)) if out is None else _dev(out, "out", torch.bfloat16, (M, p.N))
     s = _opt_f32(act_inv_s, "act_inv_s", K)
     if ws is None and (act_fp4 or s is not None):
         need = linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4)
