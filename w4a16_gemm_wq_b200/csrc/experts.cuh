@@ -319,17 +319,8 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     tmem_alloc(tmem_slot, S::TMEM_COLS);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 3) {
-    expert_tables(a, XT, bound, tstart, bad_flag);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // what needs no memory is computed while the kernel before this one ends
   const int nblocks = (a.N + 127) >> 7;
-  const int items = *bad_flag ? 0 : tstart[a.E] * nblocks;
   const int nchunks = (a.K + kExpChunk - 1) / kExpChunk;
   // this CTA's items, and its chunks of an item
   int rank = 0, c0 = 0, c1 = nchunks, first = blockIdx.x, step = gridDim.x;
@@ -340,6 +331,25 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     first /= a.split;
     step /= a.split;
   }
+  // a row's scale bytes, those of a chunk, and the alignment that all rows share
+  const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
+  const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
+  const int sc_want = FMT == GEMM_INT4 ? (kExpChunk >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 16 : 8;
+  const int sc_align = (sc_stride & 15) == 0 ? 16 : (sc_stride & 3) == 0 ? 4 : 1;
+  const int cps = S::SEG / sc_want;  // chunks of a segment
+  // stages of a chunk: whole ones, the k-blocks past K are zeros (of the codes, the scales and X)
+  const int last_stages = (a.K - (nchunks - 1) * kExpChunk + 64 * SK - 1) / (64 * SK);
+  const auto stages_of = [&](int c) { return c == nchunks - 1 ? last_stages : 4 / SK; };
+  asm volatile("" ::"r"(nblocks), "r"(c0), "r"(c1), "r"(first), "r"(step), "r"(cps), "r"(last_stages));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 3) expert_tables(a, XT, bound, tstart, bad_flag);
+  if (!a.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int items = *bad_flag ? 0 : tstart[a.E] * nblocks;
 
   struct Item {
     int e, row, rows, n0;  // expert, first row of X and their number, first weight row
@@ -356,15 +366,6 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
     it.rows = min(w, bound[lo + 1] - it.row);
     return it;
   };
-  // stages of a chunk: whole ones, the k-blocks past K are zeros (of the codes, the scales and X)
-  const int last_stages = (a.K - (nchunks - 1) * kExpChunk + 64 * SK - 1) / (64 * SK);
-  const auto stages_of = [&](int c) { return c == nchunks - 1 ? last_stages : 4 / SK; };
-  // a row's scale bytes, those of a chunk, and the alignment that all rows share
-  const uint8_t* sc_base = FMT == GEMM_INT4 ? reinterpret_cast<const uint8_t*>(a.scales) : a.bscale;
-  const int sc_stride = FMT == GEMM_INT4 ? (a.K >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? a.K >> 4 : a.K >> 5;
-  const int sc_want = FMT == GEMM_INT4 ? (kExpChunk >> a.log2g) * 2 : FMT == GEMM_NVFP4 ? 16 : 8;
-  const int sc_align = (sc_stride & 15) == 0 ? 16 : (sc_stride & 3) == 0 ? 4 : 1;
-  const int cps = S::SEG / sc_want;  // chunks of a segment
 
   if (warp == 0) {
     // ---------------------------------------------------------- codes
