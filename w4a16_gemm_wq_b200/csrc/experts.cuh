@@ -122,7 +122,9 @@ __device__ __forceinline__ int expert_of_tile(const int* tstart, int E, int tile
 // dequantized weights hold SK k-blocks each: one pair of waits and one commit of the
 // MMA issuer (about 300 clocks) for 4 SK instructions of XT / 2 clocks at most.  The same
 // shape serves few rows: an item's boxes and MMAs are as high as its rows (tiles of 64 rows
-// with deeper stages were within 2% at 13 to 1000 rows, and slower from 64 an expert on).
+// with deeper stages were within 2% at 13 to 1000 rows, and slower from 64 an expert on; of
+// 256 rows with one accumulator: 200 x 28672 x 4096 in 50 us against 66, but 100 rows of it
+// in 42 against 38, and 48 rows for each of 64 experts in 55 against 48).
 //
 // Scales are fetched for many chunks at once, SEG bytes a row, because a warp's copy
 // of 4 bytes from each of 32 rows takes as long as one of 16 bytes (about 200 clocks,
@@ -150,7 +152,10 @@ struct ExpShape {
   static_assert(A_COL + AS * SK * 32 <= TMEM_COLS, "tensor memory columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(XT % XUNIT == 0 && XUNIT % 16 == 0, "row tiles");
-  static_assert(XS >= AS, "a dequantizer waits for the stage AS back on the slots' barriers");
+  // A dequantizer waits for the stage AS back on the slots' barriers.  Where the last chunk of K has
+  // no k-block for its group, its next stage is up to 8 / SK - 1 after its last: it must have seen the
+  // slot's phase before the awaited one (of the stage XS earlier), which its parity alone could pass for.
+  static_assert(XS >= AS && XS >= 8 / SK - 1, "phases that a dequantizer may miss");
   static_assert(WS * CODE_BYTES + XS * SLOT_BYTES >= XT * 128 * 4, "a split item's fp32 partial fits the rings");
 };
 
