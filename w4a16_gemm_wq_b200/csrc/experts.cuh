@@ -292,6 +292,32 @@ __device__ __forceinline__ void dequant8_e2m1_f32(uint32_t w, float s, const flo
   for (int i = 0; i < 4; ++i) out[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
 }
 
+// What the non-finite elements of a row of X make of its product with a weight row: an infinity,
+// or NaN (0 for a row without any).  For the forms for few rows, whose own arithmetic takes away
+// what it added (INT4) or multiplies blocks of another scale by zero (MXFP4): with an infinity
+// both leave NaN where the product is one.  Read again from memory, by one thread: rare.
+template <int FMT>
+__device__ float nonfinite_terms(const ExpertArgs& a, int64_t xrow, int64_t wrow) {
+  static_assert(FMT == GEMM_INT4 || FMT == GEMM_MXFP4, "NVFP4 needs none");
+  float y = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < a.K; ++k) {
+    float x = bf16_bits_to_f32(a.X[xrow * a.K + k]);
+    if (FMT == GEMM_MXFP4 && a.inv_s) x *= a.inv_s[k];
+    if ((__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u) continue;
+    const uint32_t code = (a.packed[wrow * (a.K >> 1) + (k >> 1)] >> (4 * (k & 1))) & 15u;
+    if (FMT == GEMM_INT4) {
+      const int ng = a.K >> a.log2g, g = k >> a.log2g;
+      const uint32_t z = a.zeros ? (a.zeros[wrow * ((ng + 7) >> 3) + (g >> 3)] >> (4 * (g & 7))) & 15u : 8u;
+      y += (float(code) - float(z)) * __half2float(__ushort_as_half(a.scales[wrow * ng + g])) * x;
+    } else {
+      const uint32_t h = e2m1x2_of_byte<0>(code);
+      y += __half2float(__ushort_as_half(uint16_t(h))) * e8m0_f32(a.bscale[wrow * (a.K >> 5) + (k >> 5)]) * x;
+    }
+  }
+  return y;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertArgs a) {
   using S = ExpShape;
@@ -806,6 +832,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   __shared__ int bad_flag;
   __shared__ uint32_t rtop[kVecRows];                     // largest finite magnitude of X's rows, fp32 bits
   __shared__ float rscale[kVecRows];                      // what undoes their scaling
+  __shared__ uint32_t rbad;                               // rows that hold a non-finite value, a bit each
   float (*part)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_PART);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int K = a.K, N = a.N;
@@ -942,6 +969,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     if (staged != tile) {
       // X, or X * act_inv_s, 256 k of a row at a time: the rows' largest finite magnitudes, then the fragments
       if (threadIdx.x < kVecRows) rtop[threadIdx.x] = 0;
+      if (threadIdx.x == 0) rbad = 0;
       __syncthreads();  // also: the last run's readers are done
       const float* f = FMT == GEMM_MXFP4 ? a.inv_s : nullptr;
       // each row by two warps, alternate runs of 256 k
@@ -985,15 +1013,19 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
         }
       };
       uint32_t top = 0;
+      bool bad = false;
       pass([&](int, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
           top = max(top, b < 0x7F800000u ? b : 0u);
+          if (FMT != GEMM_NVFP4) bad |= b >= 0x7F800000u;
         }
       });
       top = __reduce_max_sync(0xffffffffu, top);
+      bad = __any_sync(0xffffffffu, bad);
       if (lane == 0) atomicMax(&rtop[m], top);
+      if (lane == 0 && bad) atomicOr(&rbad, 1u << m);
       __syncthreads();
       const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
       const float up = __uint_as_float(fe << 23);
@@ -1172,6 +1204,7 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       j = 0;
       begun = true;
     }
+    const uint32_t nonfinite = FMT == GEMM_NVFP4 ? 0u : rbad;  // this tile's: the next one is staged after the barrier
     __syncthreads();
     // ---- the warp that ends a unit begun by an earlier one adds the shares in warp order
     const int s0 = first_of(warp), us = s0 / S, ub = us * S;  // the unit of the warp's first step, and that unit's first
@@ -1192,6 +1225,17 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
         const int r = (lane + 32 * q) >> 3, m = lane & 7;
         if (m < rows && nb0 + us * 16 + r < N) {
           a.Y[int64_t(row + m) * N + nb0 + us * 16 + r] = uint16_t(pack_bf16x2(y[q], y[q]));
+        }
+      }
+    }
+    if constexpr (FMT != GEMM_NVFP4) {
+      if (nonfinite) {  // the same for every thread
+        __syncthreads();  // after the stores above
+        for (int i = threadIdx.x; i < (u1 - u0) * 16 * rows; i += kVecWarps * 32) {
+          const int m = i % rows, n = nb0 + i / rows;
+          if (!(nonfinite >> m & 1u) || n >= N) continue;
+          const float y = nonfinite_terms<FMT>(a, row + m, int64_t(e) * N + n);
+          a.Y[int64_t(row + m) * N + n] = uint16_t(pack_bf16x2(y, y));
         }
       }
     }
@@ -1247,6 +1291,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
   }
   const int64_t row0 = int64_t(e) * N + n0;
   const int rows = min(kRowRows, N - n0);  // none for the last CTA's spare warps
+  bool bad = false;  // INT4: this lane has met a non-finite activation
   float acc[kRowRows][MT];
 #pragma unroll
   for (int r = 0; r < kRowRows; ++r)
@@ -1352,7 +1397,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
           for (int i = 0; i < 4; ++i) {
             const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
             top = max(top, b < 0x7F800000u ? b : 0u);
-            if (FMT == GEMM_INT4) s += v[i];
+            if (FMT == GEMM_INT4) {
+              s += v[i];
+              bad |= b >= 0x7F800000u;
+            }
           }
         }
         const uint32_t fe = min(254u, 268u - max(top >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
@@ -1460,7 +1508,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
     if ((lane & 3) == 0) part[warp][(lane >> 2) * MT + m] = v[0];  // row lane / 4
   }
-  __syncthreads();
+  // a row of X with non-finite values: some lane of the row block's warps has met them
+  const bool nonfinite = __syncthreads_or(bad);
   const int t = threadIdx.x;
   if (t < kRowWarps / ksplit * kRowRows * MT) {
     const int b = t / (kRowRows * MT), r = t / MT % kRowRows, m = t % MT;
@@ -1468,6 +1517,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, MT == 1 ? 3 : 2)
     float y = 0.f;
     for (int w = 0; w < ksplit; ++w) y += part[b * ksplit + w][r * MT + m];
     if (FMT == GEMM_NVFP4) y *= __ldg(a.gscale + e);
+    if constexpr (FMT == GEMM_INT4) {
+      if (nonfinite && n < N) {
+        const float inf = nonfinite_terms<FMT>(a, i0 + m, int64_t(e) * N + n);
+        if (!isfinite(inf)) y = inf;
+      }
+    }
     if (n < N) a.Y[int64_t(i0 + m) * N + n] = uint16_t(pack_bf16x2(y, y));
   }
 }
