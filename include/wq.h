@@ -369,12 +369,15 @@ typedef struct {
  *            no copy of it), 4-byte aligned, not decreasing, within [0, T]
  *   Y        bf16 [T, N]; rows before offsets[0] and from offsets[E] on are
  *            left as they were
- * W4A16, fp32 accumulation, no workspace.  Up to 5 rows an expert, X may be held
- * as fp16 scaled by a power of two per row: exact down to 2^-31 of the row's
- * largest finite magnitude, to 2^-39 of it below.  An expert may hold no row or all of
- * them; T = 0 computes nothing (X, Y and offsets may then be NULL).  Offsets
- * that decrease or leave [0, T] make the call compute nothing, and the next
- * wq_device_error returns WQ_ERR_ARG. */
+ * W4A16, fp32 accumulation, no workspace.  Calls of few rows (T <= 16, or
+ * T <= 5 min(E, T)) may hold X as fp16 scaled by a power of two per row (for
+ * T <= 16 per run of 32 k): exact down to 2^-31 of the row's (run's) largest
+ * finite magnitude, to 2^-39 of it below; INT4 weights may then meet every
+ * other element of X to 2^-27 and 2^-35, and their fp32 sums are of terms of up
+ * to 1264 scale |x|.  Other calls round an INT4 weight to bf16 once.  An expert
+ * may hold no row or all of them; T = 0 computes nothing (X, Y and offsets may
+ * then be NULL).  Offsets that decrease or leave [0, T] make the call compute
+ * nothing, and the next wq_device_error returns WQ_ERR_ARG. */
 int wq_linear_experts(const wq_expert_stack* w, const uint16_t* X, int64_t T, const int32_t* offsets,
                       uint16_t* Y, void* stream);
 

@@ -1,4 +1,6 @@
-"""Values at which the forms of the expert product and the MXFP4 Linear could part: infinities."""
+"""Values at which the forms of the expert product and the MXFP4 Linear could part: infinities,
+INT4 rows of a wide range, and what few INT4 rows keep of their bits."""
+import math
 
 import numpy as np
 import pytest
@@ -65,3 +67,100 @@ def test_infinite_activations_under_scales_far_apart(lib, M):
     _same_nonfinite(Y[M - 1], _nonfinite_product(x[M - 1], mx_values(p)), "the row")
     if M > 1:
         assert_within_bound(torch.from_numpy(Y[:M - 1]), x[:M - 1], mx_values(p), False)
+
+
+def _int4_stack(lib, E, N, K, G, seed):
+    """Random codes and zero points, scales within a factor of two."""
+    g = torch.Generator().manual_seed(seed)
+    ng = K // G
+    words = lambda *s: torch.randint(-2**31, 2**31, s, generator=g).to(torch.int32).cuda()
+    zeros = words(E, N, (ng + 7) // 8)
+    if ng % 8:
+        zeros[..., -1] &= (1 << 4 * (ng % 8)) - 1
+    scales = (2.0**-7 * (1 + torch.rand(E, N, ng, generator=g))).half().cuda()
+    return lib.PackedExperts("int4", E, N, K, words(E, N, K // 8), scales=scales, zeros=zeros, group_size=G,
+                             zero_point=1)
+
+
+def _scale_of_terms(p, e):
+    """The scale of each weight, [N, K] in fp64."""
+    return np.repeat(f64(p.scales[e]), p.group_size, axis=1)
+
+
+def _int4_sum_error(p, e, x, form):
+    """Bound of the error of the fp32 sums of an INT4 row, [M, N] for x [M, K], from S = sum_k s |x_k|.
+
+    cores: per 32 k two chains of 16 multiply-adds of terms below 2 |x| (17 roundings), times 16;
+    31 adds of x times 16 + z <= 31; four more roundings of both: under 2^11 2^-24 S.
+    mma_sync: G / 16 steps of terms up to 1264 |x| (1024 + 16 * 15), each off by two units of
+    2^-23 of its partial sum at most; the sums of x times 1024 + z, 12 roundings.
+    """
+    S = np.abs(x) @ _scale_of_terms(p, e).T
+    if form == "cores":
+        return 2.0**11 * 2.0**-24 * S
+    return ((p.group_size / 16) * 2 * 1264 * 2.0**-23 + 12 * 1039 * 2.0**-24) * S
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("form", ["cores", "mma_sync"])
+def test_int4_elements_far_below_the_rows_largest(lib, G, form):
+    # group 0 holds the row's largest element and has scale 0; the elements of the other groups, 2^-34 of
+    # it, all lie between two fp16 values of the row's staging on the same side
+    counts, N = FORMS[form]
+    T, K = sum(counts), 1024
+    p = _int4_stack(lib, len(counts), N, K, G, 31)
+    p.scales[:, :, 0] = 0
+    X = torch.full((T, K), 2.0**-14 * 131 / 128, dtype=torch.bfloat16)
+    X[:, :G] = 0.0
+    X[:, 5] = 2.0**20
+    Y = f64(lib.wq_linear_experts(X.cuda(), _offsets(counts).cuda(), p))
+    x = f64(X)
+    for e in np.unique(_experts_of(counts)):
+        rows = _experts_of(counts) == e
+        w = expert_values(p, e)
+        ref = x[rows] @ w.T
+        # elements are held to 2^-35 of the row's largest
+        tol = 2.0**-8 * np.abs(ref) + 2.0**-35 * 2.0**20 * np.abs(w).sum(1) + _int4_sum_error(p, e, x[rows], form)
+        bad = np.abs(Y[rows] - ref) > tol
+        assert not bad.any(), (e, np.abs(Y[rows] - ref).max(), tol.min(), bad.mean())
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("form", ["cores", "mma_sync"])
+@pytest.mark.parametrize("outlier", [0, 64.0, 1e4])
+def test_int4_of_few_rows_rounds_no_weight(lib, G, form, outlier):
+    counts, N = FORMS[form]
+    T, K = sum(counts), 2048
+    p = _int4_stack(lib, len(counts), N, K, G, 32)
+    X = _acts(T, K, 33)
+    if outlier:
+        X[:, 77] = outlier
+        X[:, 1500] = -outlier
+        # half the weight rows have q = z under the first: its term is zero
+        z = (p.zeros[:, ::2, (77 // G) // 8] >> (4 * ((77 // G) % 8))) & 15
+        word, at = 77 // 8, 4 * (77 % 8)
+        old = p.packed[:, ::2, word]
+        p.packed[:, ::2, word] = (old & ~(15 << at)) | (z << at)
+    Y = f64(lib.wq_linear_experts(X.cuda(), _offsets(counts).cuda(), p))
+    x, err, norm = f64(X), 0.0, 0.0
+    for e in np.unique(_experts_of(counts)):
+        rows = _experts_of(counts) == e
+        ref = x[rows] @ expert_values(p, e).T
+        S = np.abs(x[rows]) @ np.abs(expert_values(p, e)).T
+        tol = 2.0**-8 * np.abs(ref) + K * 2.0**-24 * S + _int4_sum_error(p, e, x[rows], form)
+        assert (np.abs(Y[rows] - ref) <= tol).all(), e
+        err, norm = err + ((Y[rows] - ref) ** 2).sum(), norm + (ref**2).sum()
+    if not outlier:
+        # one rounding to bf16 (2^-8 at most, evenly spread) and a tenth for the sums
+        assert math.sqrt(err / norm) <= 1.1 * 2.0**-8 / math.sqrt(3), math.sqrt(err / norm)
+
+
+@pytest.mark.parametrize("fmt", ["int4_g128", "int4_g64", "int4_g32"])
+def test_int4_of_many_rows_rounds_a_weight_once(lib, fmt):
+    counts, N = FORMS["tcgen05"]
+    p = _stack(lib, fmt, len(counts), N, 2048, 34)
+    X = _acts(sum(counts), 2048, 35)
+    Y, x = f64(lib.wq_linear_experts(X.cuda(), _offsets(counts).cuda(), p)), f64(X)
+    ref = np.concatenate([x[:90] @ expert_values(p, 0).T, x[90:] @ expert_values(p, 2).T])
+    # two independent roundings to bf16, of the weights and of the result
+    assert math.sqrt(((Y - ref) ** 2).sum() / (ref**2).sum()) <= 1.1 * math.sqrt(2) * 2.0**-8 / math.sqrt(3)

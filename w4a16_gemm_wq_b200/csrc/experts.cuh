@@ -781,7 +781,8 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 //
 // X is staged once per row tile in the order of the MMA's B fragments, each row scaled
 // by a power of two that puts its largest finite magnitude at 2^14: fp16 then holds
-// bf16 exactly down to 2^-31 of that magnitude, and what is smaller to 2^-39 of it.
+// bf16 exactly down to 2^-31 of that magnitude, and what is smaller to 2^-39 of it (INT4's
+// elements that are staged / 16: 2^-27 and 2^-35).
 // Two steps at a time: one alone left the warp waiting for its own results.  Codes come
 // by cp.async, four to six steps ahead and on into the warp's next unit, into slots that
 // the copying lane reads itself (no barrier, and a loop body of two steps: one unrolled
@@ -792,8 +793,9 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 //   INT4   lane c takes G / 4 k of every group, so that an MMA stays inside a group: A is
 //          1024 + q or 1024 + 16 q (one logic instruction a pair; X of the latter staged
 //          / 16), and the group's fp32 sums lose what the 1024 and the zero point z added,
-//          P + z Q from sums of the staged X, before the fp16 scale multiplies them (the
-//          cancellation costs eight of fp32's bits, 2^-16 of the sum of magnitudes);
+//          P + z Q from sums of the staged X, before the fp16 scale multiplies them.  The
+//          sums round terms of up to 1264 |x| to fp32, about 2^-16 of the result where the
+//          |q - z| are of middling size, more where an outlier of X meets q = z;
 //   NVFP4  lane c takes 32 k in a row; A is the code times its block scale (exact);
 //   MXFP4  the same, with the block scale relative to the largest of the row's step, and
 //          the step's fp32 sums times that one; blocks under 2^-26 of it take another turn.
@@ -1044,9 +1046,14 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           w = (p * 8 / G) * WPG + (p * 8 % (G / 4)) / 8;
           o = make_uint4(pack_f16x2(v[0], v[4]), pack_f16x2(v[1] * 0.0625f, v[5] * 0.0625f), pack_f16x2(v[2], v[6]),
                          pack_f16x2(v[3] * 0.0625f, v[7] * 0.0625f));
-          // what the group's sums hold of 1024 (64 times X where it meets 16 q), and the sum of X
-          const float even = v[0] + v[4] + v[2] + v[6], odd = v[1] + v[5] + v[3] + v[7];
-          float P = 1024.f * even + 64.f * odd, Q = even + odd;
+          // what the group's sums hold of 1024, and the sum of X: both of the values as staged (those
+          // that meet 16 q are X / 16), so that a rounding of X is not multiplied by 1024
+          const auto pair = [](uint32_t h) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            return t.x + t.y;
+          };
+          const float even = pair(o.x) + pair(o.z), odd = pair(o.y) + pair(o.w);
+          float P = 1024.f * (even + odd), Q = even + 16.f * odd;
 #pragma unroll
           for (int h = 1; h < G / 8; h <<= 1) {
             P += __shfl_xor_sync(0xffffffffu, P, h);
