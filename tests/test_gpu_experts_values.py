@@ -1,5 +1,5 @@
 """Values at which the forms of the expert product and the MXFP4 Linear could part: infinities,
-INT4 rows of a wide range, and what few INT4 rows keep of their bits."""
+INT4 rows of a wide range, what few INT4 rows keep of their bits, magnitudes near the ends of fp32."""
 import math
 
 import numpy as np
@@ -164,3 +164,33 @@ def test_int4_of_many_rows_rounds_a_weight_once(lib, fmt):
     ref = np.concatenate([x[:90] @ expert_values(p, 0).T, x[90:] @ expert_values(p, 2).T])
     # two independent roundings to bf16, of the weights and of the result
     assert math.sqrt(((Y - ref) ** 2).sum() / (ref**2).sum()) <= 1.1 * math.sqrt(2) * 2.0**-8 / math.sqrt(3)
+
+
+@pytest.mark.parametrize("fmt,form,wexp,xexp", [
+    ("nvfp4", "cores", -20, 115), ("nvfp4", "cores", -100, 120), ("nvfp4", "cores", 100, -110),
+    ("mxfp4", "cores", -30, 123), ("mxfp4", "tcgen05", -30, 123), ("mxfp4", "cores", 121, -115),
+    ("mxfp4", "tcgen05", 121, -115), ("mxfp4", "cores", -115, 123), ("int4_g64", "cores", -4, 121),
+    ("int4_g32", "cores", -4, 121), ("int4_g64", "cores", -4, -118)])
+def test_magnitudes_near_the_ends_of_the_range(lib, fmt, form, wexp, xexp):
+    # finite products of factors whose exponents are far from zero
+    counts, N = FORMS[form]
+    T, K = sum(counts), 1152
+    g = torch.Generator().manual_seed(36)
+    W = (torch.randn(len(counts), N, K, generator=g).double() * 2.0**wexp).to(torch.bfloat16).cuda()
+    G = 32 if fmt == "int4_g32" else 64
+    p = lib.wq_quantize_experts(W, "int4", G) if fmt.startswith("int4") else lib.wq_quantize_experts(W, fmt)
+    X = (_acts(T, K, 37).double() * 2.0**xexp).to(torch.bfloat16)
+    Y, x = lib.wq_linear_experts(X.cuda(), _offsets(counts).cuda(), p), f64(X)
+    for e in np.unique(_experts_of(counts)):
+        rows = torch.from_numpy(_experts_of(counts) == e)
+        assert_within_bound(Y[rows.cuda()], x[rows.numpy()], expert_values(p, e), p.fmt == "int4", f"expert {e}")
+
+
+@pytest.mark.parametrize("M", [1, 2, 40])
+@pytest.mark.parametrize("wexp,xexp", [(-30, 123), (121, -115), (-115, 123), (-110, -15), (123, -130)])
+def test_mxfp4_magnitudes_near_the_ends_of_the_range(lib, M, wexp, xexp):
+    N, K = 70, 1056
+    g = torch.Generator().manual_seed(38)
+    p = lib.wq_quantize_mxfp4((torch.randn(N, K, generator=g).double() * 2.0**wexp).to(torch.bfloat16).cuda())
+    X = (_acts(M, K, 39).double() * 2.0**xexp).to(torch.bfloat16)
+    assert_within_bound(lib.wq_linear_mxfp4(X.cuda(), p), f64(X), mx_values(p), False)
