@@ -167,10 +167,13 @@ def test_int4_of_many_rows_rounds_a_weight_once(lib, fmt):
 
 
 @pytest.mark.parametrize("fmt,form,wexp,xexp", [
-    ("nvfp4", "cores", -20, 115), ("nvfp4", "cores", -100, 120), ("nvfp4", "cores", 100, -110),
-    ("mxfp4", "cores", -30, 123), ("mxfp4", "tcgen05", -30, 123), ("mxfp4", "cores", 121, -115),
-    ("mxfp4", "tcgen05", 121, -115), ("mxfp4", "cores", -115, 123), ("int4_g64", "cores", -4, 121),
-    ("int4_g32", "cores", -4, 121), ("int4_g64", "cores", -4, -118)])
+    ("nvfp4", "cores", -20, 115), ("nvfp4", "mma_sync", -20, 115), ("nvfp4", "cores", -100, 120),
+    ("nvfp4", "mma_sync", -100, 120), ("nvfp4", "cores", 100, -110), ("nvfp4", "mma_sync", 100, -110),
+    ("mxfp4", "cores", -30, 123), ("mxfp4", "mma_sync", -30, 123), ("mxfp4", "tcgen05", -30, 123),
+    ("mxfp4", "cores", 121, -115), ("mxfp4", "mma_sync", 121, -115), ("mxfp4", "tcgen05", 121, -115),
+    ("mxfp4", "cores", -115, 123), ("mxfp4", "mma_sync", -115, 123), ("mxfp4", "mma_sync", -110, -15),
+    ("int4_g64", "cores", -4, 121), ("int4_g32", "cores", -4, 121), ("int4_g64", "mma_sync", -4, 121),
+    ("int4_g64", "cores", -4, -118), ("int4_g64", "mma_sync", -4, -118)])
 def test_magnitudes_near_the_ends_of_the_range(lib, fmt, form, wexp, xexp):
     # finite products of factors whose exponents are far from zero
     counts, N = FORMS[form]
@@ -186,7 +189,7 @@ def test_magnitudes_near_the_ends_of_the_range(lib, fmt, form, wexp, xexp):
         assert_within_bound(Y[rows.cuda()], x[rows.numpy()], expert_values(p, e), p.fmt == "int4", f"expert {e}")
 
 
-@pytest.mark.parametrize("M", [1, 2, 40])
+@pytest.mark.parametrize("M", [1, 2, 5, 8, 40])
 @pytest.mark.parametrize("wexp,xexp", [(-30, 123), (121, -115), (-115, 123), (-110, -15), (123, -130)])
 def test_mxfp4_magnitudes_near_the_ends_of_the_range(lib, M, wexp, xexp):
     N, K = 70, 1056

@@ -833,7 +833,9 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
   __shared__ int bound[kMaxExperts + 4], tstart[kMaxExperts + 4];
   __shared__ int bad_flag;
   __shared__ uint32_t rtop[kVecRows];                     // largest finite magnitude of X's rows, fp32 bits
-  __shared__ float rscale[kVecRows];                      // what undoes their scaling
+  // what undoes their scaling; MXFP4's sums are kept within fp32 by taking 2^-64 to 2^64 of it (rundo)
+  // with each step's scales and only the rest (rscale) at the end
+  __shared__ float rscale[kVecRows], rundo[kVecRows];
   __shared__ uint32_t rbad;                               // rows that hold a non-finite value, a bit each
   float (*part)[16][kVecRows] = reinterpret_cast<float (*)[16][kVecRows]>(vec_smem + V::OFF_PART);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -1031,7 +1033,13 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
       __syncthreads();
       const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
       const float up = __uint_as_float(fe << 23);
-      if (lane == 0) rscale[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
+      if (FMT == GEMM_MXFP4) {
+        const uint32_t fu = min(191u, max(63u, fe));  // 127 -+ 64
+        if (lane == 0) rundo[m] = __uint_as_float((254u - fu) << 23);
+        if (lane == 0) rscale[m] = __uint_as_float((127u + fu - fe) << 23);
+      } else if (lane == 0) {
+        rscale[m] = __uint_as_float(fe == 254u ? 0x00400000u : (254u - fe) << 23);
+      }
       pass([&](int k, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= up;
@@ -1073,6 +1081,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
     }
 
     // ---- the warp's steps
+    // MXFP4: a step's sums, below 2^38, meet what undoes the scaling of columns 2 c and 2 c + 1 before
+    // their scale of up to 2^127
+    const float undo0 = FMT == GEMM_MXFP4 ? 0x1p-13f * rundo[2 * c] : 0.f;
+    const float undo1 = FMT == GEMM_MXFP4 ? 0x1p-13f * rundo[2 * c + 1] : 0.f;
     // one step's products from its codes, scales and fragments
     const auto products = [&](int j, const uint4& cl4, const uint4& ch4, const Scales& r, float (&acc)[4]) {
       const uint32_t wl[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, wh[4] = {ch4.x, ch4.y, ch4.z, ch4.w};
@@ -1147,10 +1159,10 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
             mmas(fl * 0x10001u, fl * 0x10001u, fh * 0x10001u, fh * 0x10001u, d);
             // 2^(top - 127 - 13) in two factors: it may lie outside fp32's normal range
             const float ml = e8m0_f32(min(254u, max(tl, 1u) - 1u)), mh = e8m0_f32(min(254u, max(th, 1u) - 1u));
-            acc[0] = fmaf(d[0] * 0x1p-13f, ml, acc[0]);
-            acc[1] = fmaf(d[1] * 0x1p-13f, ml, acc[1]);
-            acc[2] = fmaf(d[2] * 0x1p-13f, mh, acc[2]);
-            acc[3] = fmaf(d[3] * 0x1p-13f, mh, acc[3]);
+            acc[0] = fmaf(d[0] * undo0, ml, acc[0]);
+            acc[1] = fmaf(d[1] * undo1, ml, acc[1]);
+            acc[2] = fmaf(d[2] * undo0, mh, acc[2]);
+            acc[3] = fmaf(d[3] * undo1, mh, acc[3]);
             rest = (inl ? 0u : rl) | ((inh ? 0u : rh) << 16);
           };
           turn();
@@ -1198,7 +1210,13 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int m = 2 * c + (q & 1), r = g + (q >> 1) * 8;
-        const float y = (acc[q] + acc2[q]) * rscale[m] * gmul;
+        float y = acc[q] + acc2[q];
+        if (FMT != GEMM_NVFP4) {
+          y *= rscale[m];
+        } else {  // one large and the other small: their product first
+          const bool apart = (gmul > 1.f) != (rscale[m] > 1.f);
+          y = apart ? y * (gmul * rscale[m]) : y * gmul * rscale[m];
+        }
         acc[q] = acc2[q] = 0.f;
         // slot 2 w: the unit was begun by an earlier warp; 2 w + 1: by this one
         if (!whole) {
