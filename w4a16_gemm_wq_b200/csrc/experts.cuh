@@ -295,9 +295,10 @@ __device__ __forceinline__ void dequant8_e2m1_f32(uint32_t w, float s, const flo
 // What the non-finite elements of a row of X make of its product with a weight row: an infinity,
 // or NaN (0 for a row without any).  For the forms for few rows, whose own arithmetic takes away
 // what it added (INT4) or multiplies blocks of another scale by zero (MXFP4): with an infinity
-// both leave NaN where the product is one.  Read again from memory, by one thread: rare.
+// both leave NaN where the product is one.  Read again from memory, by one thread: rare, and
+// out of line for the registers and the length of what is not.
 template <int FMT>
-__device__ float nonfinite_terms(const ExpertArgs& a, int64_t xrow, int64_t wrow) {
+__device__ __noinline__ float nonfinite_terms(const ExpertArgs& a, int64_t xrow, int64_t wrow) {
   static_assert(FMT == GEMM_INT4 || FMT == GEMM_MXFP4, "NVFP4 needs none");
   float y = 0.f;
 #pragma unroll 1
@@ -1016,20 +1017,23 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
           }
         }
       };
-      uint32_t top = 0;
-      bool bad = false;
-      pass([&](int, float (&v)[8]) {
+      const auto largest = [&](uint32_t below) {  // of the magnitudes under `below`, fp32 bits
+        uint32_t top = 0;
+        pass([&](int, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-          top = max(top, b < 0x7F800000u ? b : 0u);
-          if (FMT != GEMM_NVFP4) bad |= b >= 0x7F800000u;
-        }
-      });
-      top = __reduce_max_sync(0xffffffffu, top);
-      bad = __any_sync(0xffffffffu, bad);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+            top = max(top, b < below ? b : 0u);
+          }
+        });
+        return __reduce_max_sync(0xffffffffu, top);
+      };
+      uint32_t top = largest(0x80000000u);
+      if (top >= 0x7F800000u) {  // rare: a second look for the finite ones
+        if (lane == 0) atomicOr(&rbad, 1u << m);
+        top = largest(0x7F800000u);
+      }
       if (lane == 0) atomicMax(&rtop[m], top);
-      if (lane == 0 && bad) atomicOr(&rbad, 1u << m);
       __syncthreads();
       const uint32_t fe = min(254u, 268u - max(rtop[m] >> 23, 1u));  // exponent field of 2^14 / 2^floor(log2 top)
       const float up = __uint_as_float(fe << 23);
