@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests._linear_ref import assert_within_bound, expert_values, f64, mx_values
-from tests.test_gpu_experts import FMTS, _acts, _offsets, _stack
+from tests.test_gpu_experts import FMTS, _acts, _offsets, _run, _stack
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,21 @@ def test_mxfp4_magnitudes_near_the_ends_of_the_range(lib, M, wexp, xexp):
     p = lib.wq_quantize_mxfp4((torch.randn(N, K, generator=g).double() * 2.0**wexp).to(torch.bfloat16).cuda())
     X = (_acts(M, K, 39).double() * 2.0**xexp).to(torch.bfloat16)
     assert_within_bound(lib.wq_linear_mxfp4(X.cuda(), p), f64(X), mx_values(p), False)
+
+
+@pytest.mark.parametrize("N,K", [(150, 512), (2051, 2048)])
+def test_one_expert_is_the_plain_product(lib, N, K):
+    # one expert that holds all rows runs as the product without offsets does: the same bits
+    p = _stack(lib, "mxfp4", 1, N, K, 51)
+    one = lib.PackedMXFP4(p.packed[0], p.bscale[0], N, K)
+    for M in (1, 2, 3, 5, 8, 9, 13, 16, 17, 40):
+        X = _acts(M, K, M).cuda()
+        Y = lib.wq_linear_experts(X, _offsets([M]).cuda(), p)
+        assert torch.equal(Y.view(torch.int16), lib.wq_linear_mxfp4(X, one).view(torch.int16)), M
+
+
+@pytest.mark.parametrize("fmt", ["int4_g64", "int4_g32", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N,K", [(2100, 4096), (4099, 2112), (700, 7168)])
+@pytest.mark.parametrize("counts", [[0, 1, 0, 0, 0, 0, 1, 0], [3, 0, 1, 2, 0, 4, 1, 5], [0, 0, 16, 0, 0, 0, 0, 0]])
+def test_few_rows_of_few_large_experts(lib, fmt, N, K, counts):
+    _run(lib, _stack(lib, fmt, len(counts), N, K, 52), counts, 53, 0, 0)

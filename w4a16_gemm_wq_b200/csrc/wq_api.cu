@@ -741,16 +741,53 @@ int launch_expert_rows(const wq::ExpertArgs& a, cudaStream_t st) {
   return !a.offsets && a.T == 2 ? launch_expert_rows_mt<FMT, 2>(a, st) : launch_expert_rows_mt<FMT, 1>(a, st);
 }
 
-// Which form runs (all three where it says; microseconds, MXFP4 unless it says INT4):
-//   CUDA cores: few rows of which no expert is likely to hold several (up to 16), or the one or
-//     two rows of a plain product while there are few weights to convert for each row (2^25), or
-//     where K is too long for the mma.sync form.
+// Whether up to 16 rows over several experts take the CUDA-core form, which converts an expert's
+// weights again for every row.  The other forms convert them once a holder: A = E (1 - (1 - 1/E)^T)
+// experts hold any of T rows routed alike.  In units of a weight's conversion on the CUDA cores the
+// mma.sync form takes 5/6 of one a weight and holder, the tcgen05 form (K too long for that one)
+// 3/2, and their longer start is worth `ahead` weights.  Best of the other two forms /
+// cores, microseconds, top-2 routing over 8 experts, top-8 over 64 and 128:
+//                         rows   INT4 (G = 64)   NVFP4         MXFP4
+//   8 x 1408 x 2048         8   12.0 / 7.8      10.4 / 6.8    11.6 / 8.2
+//                          12   12.0 / 10.2     10.4 / 9.0    11.6 / 10.9
+//                          16   12.0 / 12.3     10.6 / 11.0   11.6 / 13.2
+//   64 x 1408 x 2048        8   13.0 / 9.1      11.8 / 8.0    12.8 / 9.5
+//                          16   18.4 / 14.4     16.6 / 12.6   18.6 / 14.7
+//   128 x 4096 x 2048       4   13.7 / 11.6     13.1 / 10.4   13.7 / 12.1
+//                           8   21.3 / 18.6     18.5 / 16.5   20.8 / 19.4
+//                          16   30.6 / 33.1     25.5 / 28.4   29.7 / 32.6
+//   8 x 4096 x 4096         2   14.6 / 11.9     12.5 / 10.8   13.8 / 12.4
+//                           4   20.6 / 18.2     19.2 / 16.1   20.3 / 19.7
+//                           8   28.2 / 32.2     22.9 / 27.4   25.9 / 32.0
+//                          16   31.8 / 59.3     25.7 / 49.1   29.4 / 56.7
+//   8 x 14336 x 4096        1   19.3 / 17.6     15.4 / 15.2   17.4 / 18.0
+//                           2   31.8 / 30.0     25.0 / 25.6   29.1 / 30.6
+//                           4   47.3 / 54.5     35.7 / 45.2   42.0 / 54.2
+//                          16   77.1 / 197      56.6 / 160    66.9 / 186
+//   8 x 4096 x 14336        4   57.6 / 51.1     53.8 / 43.9   56.0 / 54.8
+//                           8   101 / 94.7      86.2 / 79.6   97.9 / 99.9
+//                          16   108 / 179       92.1 / 147    105 / 183
+template <int FMT>
+bool expert_rows_pay(const wq::ExpertArgs& a) {
+  if (a.T > 16) return false;
+  double none = 1;  // the chance of an expert to hold no row
+  for (int t = 0; t < a.T; ++t) none *= 1 - 1.0 / a.E;
+  const double once = expert_gemv_serves<FMT>(a.K) ? 5.0 / 6 : 1.5;
+  const double ahead = FMT == wq::GEMM_INT4 ? 21e6 : FMT == wq::GEMM_NVFP4 ? 24e6 : 14e6;
+  return (a.T - once * a.E * (1 - none)) * a.N * a.K <= ahead;
+}
+
+// Which form runs (all three where it says; microseconds, MXFP4 unless it says INT4).  One expert
+// that holds all rows is a plain product.
+//   CUDA cores: up to 16 rows over several experts by the rule above; the one or two rows of a
+//     plain product while there are few weights to convert for each row (2^25), or where K is
+//     too long for the mma.sync form.
 //       plain, N x K of W            2048 x 2048   11008 x 2048   28672 x 4096   2048 x 11008
 //         1 row   cores / mma.sync    4.7 / 6.4     8.7 / 9.2      28 / 25        11.7 / 14.0
 //         2 rows                      5.1 / 6.4    11.7 / 9.3      40 / 25        10.7 / 14.1
-//       64 experts of 1408 x 2048     8 rows: 9.6 / 16.0, 16: 14.7 / 19.0, 32: 25 / 26
-//   mma.sync: at most 8 rows of a plain product; at most 5 rows a holder, where the tcgen05 form
-//     has more items than one wave.  K up to 6656 (INT4 5888): longer ones, shared by a cluster,
+//   mma.sync: at most 8 rows of a plain product; at most 5 min(E, T) rows over several experts (the
+//     host does not know which of them hold rows), where the tcgen05 form has more items than one
+//     wave.  K up to 6656 (INT4 5888): longer ones, shared by a cluster,
 //     measured slower than the tcgen05 form.
 //       plain, mma.sync / tcgen05     3 rows: 9.4 / 12.2 of 11008 x 2048, 25 / 36 of 28672 x 4096
 //                                     8 rows: 10.2 / 12.3, 27 / 36, and (as a cluster) 16.7 / 14.9 of
@@ -763,7 +800,7 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   wq::ExpertArgs v = a;
   v.X = X; v.packed = static_cast<const uint8_t*>(packed);
   const bool serves = expert_gemv_serves<FMT>(a.K);
-  if (a.offsets ? a.T <= 16 : a.T <= 2 && (!serves || int64_t(a.T) * a.N * a.K <= 1 << 25))
+  if (a.E > 1 ? expert_rows_pay<FMT>(a) : a.T <= 2 && (!serves || int64_t(a.T) * a.N * a.K <= 1 << 25))
     return launch_expert_rows<FMT>(v, st);
   const bool few = a.E == 1 ? a.T <= wq::kVecRows
                             : a.T <= 5 * std::min(a.E, a.T) && expert_items(a) > wq::kTcMaxCtas;
