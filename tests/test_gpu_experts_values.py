@@ -215,3 +215,100 @@ def test_one_expert_is_the_plain_product(lib, N, K):
 @pytest.mark.parametrize("counts", [[0, 1, 0, 0, 0, 0, 1, 0], [3, 0, 1, 2, 0, 4, 1, 5], [0, 0, 16, 0, 0, 0, 0, 0]])
 def test_few_rows_of_few_large_experts(lib, fmt, N, K, counts):
     _run(lib, _stack(lib, fmt, len(counts), N, K, 52), counts, 53, 0, 0)
+
+
+# few rows of many experts: the mma.sync form
+MANY = dict(E=40, N=525, K=512)
+
+
+def _many(lib, fmt, seed):
+    return _stack(lib, fmt, MANY["E"], MANY["N"], MANY["K"], seed)
+
+
+@pytest.mark.parametrize("fmt", ["int4_g64", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("change", [(3, -1), (20, 0), (7, 1 << 30), (40, 61), (0, 5)])
+def test_bad_offsets_of_many_experts_compute_nothing(lib, fmt, change):
+    p, T = _many(lib, fmt, 41), 60
+    offsets = torch.tensor([i * T // 40 for i in range(41)], dtype=torch.int32)
+    offsets[change[0]] = change[1]
+    out = torch.full((T, p.N), 3.0, dtype=torch.bfloat16, device="cuda")
+    lib.wq_linear_experts(_acts(T, p.K, 1).cuda(), offsets.cuda(), p, out=out)
+    with pytest.raises(lib.WQError) as e:
+        lib.wq_device_error()
+    assert e.value.status == lib.WQ_ERR_ARG and "offsets" in str(e.value)
+    assert (out == 3.0).all() and lib.wq_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_experts_give_the_same_bits_every_time(lib, fmt):
+    p, counts = _many(lib, fmt, 42), [0, 1, 2, 3] * 10
+    X, o = _acts(sum(counts), p.K, 2).cuda(), _offsets(counts).cuda()
+    ys = [lib.wq_linear_experts(X, o, p).view(torch.int16) for _ in range(4)]
+    assert all(torch.equal(ys[0], y) for y in ys[1:])
+
+
+@pytest.mark.parametrize("M", [5, 8])
+def test_nan_scale_of_a_block_stays_in_its_column(lib, M):
+    N, K = 140, 320
+    p = lib.wq_quantize_mxfp4((torch.randn(N, K, generator=torch.Generator().manual_seed(1)) / 16).to(torch.bfloat16).cuda())
+    p.bscale[17, 4] = 255
+    p.codes[33, 32:48] = 0  # a block of zeros under a NaN scale is NaN too
+    p.bscale[33, 2] = 255
+    X = _acts(M, K, 3)
+    X[2, 9] = float("nan")
+    Y = f64(lib.wq_linear_mxfp4(X.cuda(), p))
+    assert np.isnan(Y[:, [17, 33]]).all() and np.isnan(Y[2]).all()
+    cols = ~np.isin(np.arange(N), [17, 33])
+    assert np.isfinite(Y[np.ix_(np.arange(M) != 2, cols)]).all()
+
+
+def test_nan_scale_of_one_of_many_experts(lib):
+    p, counts = _many(lib, "mxfp4", 43), [1, 2] * 20
+    p.bscale[7, 11, 3] = 255
+    T = sum(counts)
+    Y = f64(lib.wq_linear_experts(_acts(T, p.K, 3).cuda(), _offsets(counts).cuda(), p))
+    mine = _experts_of(counts) == 7
+    assert np.isnan(Y[mine, 11]).all()
+    Y[mine, 11] = 0
+    assert np.isfinite(Y).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4_g64", "nvfp4", "mxfp4"])
+def test_many_experts_replayed_with_other_offsets_and_on_two_streams(lib, fmt):
+    p, T = _many(lib, fmt, 44), 60
+    X, o = _acts(T, p.K, 1).cuda(), _offsets([0, 1, 2, 3] * 10).cuda()
+    outs = [torch.zeros(T, p.N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        lib.wq_linear_experts(X, o, p, out=outs[0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            lib.wq_linear_experts(X, o, p, out=outs[0])
+    torch.cuda.current_stream().wait_stream(st)
+
+    def check(Y, X, counts):
+        r = 0
+        for e, n in enumerate(counts):
+            if n:
+                assert_within_bound(Y[r:r + n], f64(X[r:r + n]), expert_values(p, e), p.fmt == "int4", f"expert {e}")
+            r += n
+
+    sizes = [[60] + [0] * 39, [0] * 39 + [60], [3, 0] * 20, [0] * 40, [1, 2, 1, 2] * 10]
+    for i, counts in enumerate(sizes):
+        outs[0].fill_(5.0)
+        X.copy_(_acts(T, p.K, i + 5))
+        o.copy_(_offsets(counts))
+        g.replay()
+        check(outs[0], X, counts)
+        assert (outs[0][sum(counts):] == 5.0).all()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s, y in zip(streams, outs):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                lib.wq_linear_experts(X, o, p, out=y)
+    torch.cuda.synchronize()
+    assert lib.wq_device_error() == 0
+    check(outs[0], X, sizes[-1])
+    assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
