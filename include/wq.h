@@ -57,7 +57,9 @@
  * E2M1 elements, one E8M0 scale per block of 32; the pages have no counterpart):
  *    codes   uint8 [N, K/2]    nibbles as NVFP4
  *    bscale  uint8 [N, K/32]   E8M0 block scale: 2^(byte - 127), 255 = NaN
- *    w_hat = e2m1(code) * 2^(bscale - 127), exact in bf16
+ *    w_hat = e2m1(code) * 2^(bscale - 127), exact in bf16 below 2^128; values
+ *    from there on (bytes 253 and 254, which the pack never writes) may count
+ *    as infinities
  */
 #ifndef WQ_H_
 #define WQ_H_
@@ -165,7 +167,7 @@ int wq_quantize_mxfp4(const uint16_t* W, int64_t N, int64_t K, const float* scal
                       uint8_t* bscale, void* stream);
 
 /* wq_dequantize_mxfp4 -- the values an MXFP4 pack stands for, W bf16 [N, K]
- * (exact; NaN under a NaN scale, and an infinity where 6 * 2^126 or more is
+ * (exact; NaN under a NaN scale, and an infinity where 2^128 or more is
  * stored, which wq_quantize_mxfp4 never does). */
 int wq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* bscale, int64_t N, int64_t K, uint16_t* W,
                         void* stream);
@@ -335,7 +337,8 @@ int wq_linear_nvfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
  *   act_fp4 = 0: W4A16, activations stay bf16.  With act_inv_s each term is
  *            rounded to bf16 once, as X * act_inv_s (given the workspace of
  *            wq_linear_workspace_size) or as the weight times act_inv_s
- *            (without).  Sizes that ask for no workspace hold
+ *            (without), which has to stay within bf16's range.  Sizes that ask
+ *            for no workspace hold
  *            X * act_inv_s to 2^-11 instead, as fp16 scaled by a power of
  *            two per row (of a run of 32 k for M <= 2): below 2^-39 of the
  *            row's (run's) largest finite magnitude it counts as zero.
@@ -374,7 +377,10 @@ typedef struct {
  * T <= 16 per run of 32 k): exact down to 2^-31 of the row's (run's) largest
  * finite magnitude, to 2^-39 of it below; INT4 weights may then meet every
  * other element of X to 2^-27 and 2^-35, and their fp32 sums are of terms of up
- * to 1264 scale |x|.  Other calls round an INT4 weight to bf16 once.  An expert
+ * to 1264 scale |x|.  Other calls round an INT4 weight to bf16 once (2^-8 of it
+ * at most), and their fp32 sums are of 16 w x (INT4) or of w x / global_scale
+ * (NVFP4): activations from about 2^100 on may leave fp32 there.  Infinities and
+ * NaN in a row of X make of its outputs what the product does.  An expert
  * may hold no row or all of them; T = 0 computes nothing (X, Y and offsets may
  * then be NULL).  Offsets that decrease or leave [0, T] make the call compute
  * nothing, and the next wq_device_error returns WQ_ERR_ARG. */

@@ -31,9 +31,9 @@
 // chunk of 256 k takes 8 clocks a row of X in the tensor pipe, and about 1900 clocks to
 // convert and store, whatever its rows; what a chunk's four dequantizer warps of a scheduler
 // wait for does not overlap (two chunks a wait, or the groups started apart, measured the same).
-// 2048 x 11008 x 2048 MXFP4: 70.6 us, 1308 TFLOP/s (tensor pipe 70% busy, issue 65%; without
-// conversions and their store 58.8 us); 16384 rows over 64 NVFP4 experts of 1408 x 2048: 95 us,
-// 993 TFLOP/s; 13 x 28672 x 4096: 36 us.
+// 2048 x 11008 x 2048 MXFP4: 70.2 us, 1316 TFLOP/s (tensor pipe 70% busy, issue 65%; without
+// conversions and their store 58.8 us); 16384 rows over 64 NVFP4 experts of 1408 x 2048: 94 us,
+// 1002 TFLOP/s; 13 x 28672 x 4096: 36 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kExpThreads, 1) expert_gemm_kernel(const __gri
 // (0.53 to 0.63 bytes a weight) and by the instructions of the dequantization, which
 // is why both operands are fp16: a pair of E2M1 codes is one conversion and one product
 // there, against one conversion, two multiply-adds and a packing in bf16.  256 rows over 64
-// experts of 1408 x 2048: INT4 (G = 64) 40.5 us, 2.4 TB/s; MXFP4 38 us; NVFP4 34 us (issue
+// experts of 1408 x 2048: INT4 (G = 64) 41 us, 2.4 TB/s; MXFP4 39.7 us; NVFP4 34.6 us (issue
 // slots 50% busy, DRAM 28%: four warps a scheduler, dependent conversions and MMAs).
 //
 // A unit is 16 weight rows of one row tile; a step of it is 128 k.  A CTA takes a
@@ -1273,11 +1273,12 @@ __global__ void __launch_bounds__(kVecWarps * 32, 1) expert_gemv_kernel(const __
 }
 
 // ---------------------------------------------------------------------------
-// One or two rows of X per product: multiply-adds on the CUDA cores, which take fewer
+// Few rows, each by itself: multiply-adds on the CUDA cores, which take fewer
 // instructions a weight here (1.5 to 2, and one more for a second row) than the MMA form
 // above (about 2.5), need no staging and no barrier before the weights are under way.  One
-// row of 11008 x 2048 MXFP4: 8.6 us, 1.4 TB/s (the launch and two dependent trips to memory
-// are half of it: 2048 x 2048 takes 4.4 us); 8 rows over 64 experts of 1408 x 2048: 9.5 us.
+// row of 11008 x 2048 MXFP4: 8.7 us, 1.4 TB/s (the launch and two dependent trips to memory
+// are half of it: 2048 x 2048 takes 4.6 us); 8 rows over 64 experts of 1408 x 2048: MXFP4 9.5 us,
+// INT4 9.3, NVFP4 8.2.
 //
 // A warp takes 8 weight rows over every `ksplit`-th 1024 k (lane: 32 consecutive k, 16
 // bytes a row), all rows' codes by cp.async into slots that the lane reads itself, which

@@ -97,9 +97,10 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_pack_kernel(const uint16_t* 
   }
 }
 
-// X 1/s in bf16, for the W4A16 product: one rounding of 2^-9 a term, as the product would
+// X 1/s in bf16, for the W4A16 product: one rounding of 2^-8 at most a term, as the product would
 // otherwise round the weight times 1/s, but once an element of X instead of once for every
-// weight in every row tile.
+// weight in every row tile (bf16 because the MMA takes both operands in one type, and fp16 has
+// no room for the weights' scales; a second bf16 term for the rest would double the products).
 __global__ void __launch_bounds__(kMxThreads) mxfp4_scale_kernel(const uint16_t* __restrict__ X,
                                                                  const float* __restrict__ s, uint64_t words,
                                                                  uint32_t row_words, uint16_t* __restrict__ out) {
@@ -119,8 +120,8 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_scale_kernel(const uint16_t*
   }
 }
 
-// The values of a pack in bf16: exact (at most two significant bits, exponents -128 .. 129; a
-// scale byte of 254, which the pack never writes, may overflow to infinity).
+// The values of a pack in bf16: exact (at most two significant bits, exponents -128 .. 129; under
+// scale bytes of 253 and 254, which the pack never writes, codes of 2^128 and more are infinities).
 __global__ void __launch_bounds__(kMxThreads) mxfp4_unpack_kernel(const uint32_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ bscale, uint64_t words,
                                                                   uint16_t* __restrict__ out) {

@@ -783,17 +783,18 @@ bool expert_rows_pay(const wq::ExpertArgs& a) {
 //     plain product while there are few weights to convert for each row (2^25), or where K is
 //     too long for the mma.sync form.
 //       plain, N x K of W            2048 x 2048   11008 x 2048   28672 x 4096   2048 x 11008
-//         1 row   cores / mma.sync    4.7 / 6.4     8.7 / 9.2      28 / 25        11.7 / 14.0
-//         2 rows                      5.1 / 6.4    11.7 / 9.3      40 / 25        10.7 / 14.1
+//         1 row   cores / mma.sync    4.7 / 6.1     8.7 / 9.1      29 / 25        11.8 / (tcgen05) 13.6
+//         2 rows                      5.9 / 6.2    11.8 / 9.2      40 / 25        10.5 / 13.6
 //   mma.sync: at most 8 rows of a plain product; at most 5 min(E, T) rows over several experts (the
 //     host does not know which of them hold rows), where the tcgen05 form has more items than one
-//     wave.  K up to 6656 (INT4 5888): longer ones, shared by a cluster,
-//     measured slower than the tcgen05 form.
-//       plain, mma.sync / tcgen05     3 rows: 9.4 / 12.2 of 11008 x 2048, 25 / 36 of 28672 x 4096
-//                                     8 rows: 10.2 / 12.3, 27 / 36, and (as a cluster) 16.7 / 14.9 of
-//                                     2051 x 11008; 64 experts of 2048 x 11008, 128 rows: 351 / 292
-//       1408 x 2048, 64 experts       64 rows: 38 / 46 (INT4 44 / 46), 256 rows: 41 / 46 (INT4 46 / 46)
-//                    8 experts        24 rows: 15.6 / 12.8
+//     wave.  K up to 6656 (INT4 5888), whose rows fit shared memory: sharing a longer one in a
+//     cluster measured slower than the tcgen05 form (8 rows of 2051 x 11008: 16.7 / 14.9).
+//       plain, mma.sync / tcgen05     3 rows: 9.3 / 11.3 of 11008 x 2048, 25 / 34 of 28672 x 4096
+//                                     8 rows: 10.1 / 11.4, 27 / 34
+//       1408 x 2048, 64 experts       64 rows: 28.8 / 29.5 (INT4 29.6 / 30.1, NVFP4 25.2 / 26.8)
+//                                     256 rows: 39.7 / 44.8 (INT4 40.9 / 45.6, NVFP4 34.6 / 40.8)
+//                    8 experts        24 rows: 14.2 / 12.3
+//       2048 x 6656, 64 experts       128 rows: 159 / 151
 //   tcgen05: the rest.
 template <int FMT>
 int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* packed, cudaStream_t st) {
@@ -1777,8 +1778,8 @@ int wq_linear_mxfp4(const uint16_t* X, int64_t M, int64_t N, int64_t K, const ui
     f.M = int(M); f.N = int(N); f.K = int(K);
     return launch_mxf4(f, wsb + L.off_codes, codes, st);
   }
-  // X 1/s first, where there is room for it (2048 x 11008 x 2048: 80.6 us against 106, 13 x 2051 x
-  // 11008: 19.7 against 21.9); the weights take 1/s otherwise.
+  // X 1/s first, where there is room for it (2048 x 11008 x 2048: 74.4 us against 112, 13 x 2051 x
+  // 11008: 14.9 against 21.4; 69.9 and 13.9 without 1/s); the weights take 1/s otherwise.
   if (act_inv_s && mx_scales_x(M, K) && ws && ws_bytes >= size_t(M) * size_t(K) * 2) {
     REQUIRE_PTR(ws);
     const uint64_t words = uint64_t(M) * uint64_t(K / 8);
