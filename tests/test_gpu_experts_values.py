@@ -312,3 +312,19 @@ def test_many_experts_replayed_with_other_offsets_and_on_two_streams(lib, fmt):
     assert lib.wq_device_error() == 0
     check(outs[0], X, sizes[-1])
     assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def test_binding_refuses_workspaces_and_group_items_it_cannot_hold(lib):
+    X, W = _acts(12, 64, 1).cuda(), _acts(16, 64, 2).cuda()
+    p = lib.wq_quantize_mxfp4(W)
+    need = lib.linear_workspace_size(12, 16, 64, lib.WQ_FMT_MXFP4, 1)
+    out = torch.empty(12, 16, dtype=torch.bfloat16, device="cuda")
+    short = lib.PackedMXFP4(p.codes, p.bscale[:, :1].contiguous(), 16, 64)
+    bad = [lambda: lib.wq_linear_mxfp4(X, p, act_fp4=1, ws=torch.empty(1, dtype=torch.uint8, device="cuda").expand(need)),
+           lambda: lib.wq_linear_mxfp4(X, p, act_fp4=1, ws=torch.empty(need, dtype=torch.uint8)),
+           lambda: lib.make_group([(X, short, out)]),
+           lambda: lib.make_group([(X, lib.wq_quantize_experts(W.view(1, 16, 64)), out)])]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()

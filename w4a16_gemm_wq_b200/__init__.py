@@ -599,6 +599,8 @@ def wq_linear_mxfp4(X: torch.Tensor, p: PackedMXFP4, act_fp4: int = 0, act_inv_s
     if ws is None and (act_fp4 or s is not None):
         need = linear_workspace_size(M, p.N, K, WQ_FMT_MXFP4, act_fp4)
         ws = X.new_empty(need, dtype=torch.uint8) if need else None
+    elif ws is not None:
+        _dev(ws, "ws")  # a strided or expanded one holds fewer bytes than its elements count
     _call("wq_linear_mxfp4", _device_of(X, p.codes, p.bscale, Y, s, ws), X.data_ptr(), M, p.N, K, p.codes.data_ptr(),
           p.bscale.data_ptr(), act_fp4, _addr(s), Y.data_ptr(), _addr(ws),
           0 if ws is None else ws.numel() * ws.element_size())
@@ -688,7 +690,10 @@ def make_group(calls):
             it.zeros = None if p.zeros is None else p.zeros.data_ptr()
             it.group_size, it.zero_point = p.group_size, p.zero_point
         elif isinstance(p, PackedMXFP4):
+            _mx_pack(p)
             it.format, it.packed, it.bscale = WQ_FMT_MXFP4, p.codes.data_ptr(), p.bscale.data_ptr()
+        elif isinstance(p, PackedExperts):
+            raise ValueError(f"item {i}: a stack of experts is no item of a group: wq_linear_experts")
         else:
             it.format, it.packed = WQ_FMT_NVFP4, p.codes.data_ptr()
             it.bscale, it.global_scale = p.bscale.data_ptr(), p.global_scale.data_ptr()
