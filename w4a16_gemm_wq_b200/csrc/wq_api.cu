@@ -741,7 +741,7 @@ int launch_expert_rows(const wq::ExpertArgs& a, cudaStream_t st) {
   return !a.offsets && a.T == 2 ? launch_expert_rows_mt<FMT, 2>(a, st) : launch_expert_rows_mt<FMT, 1>(a, st);
 }
 
-// Whether up to 16 rows over several experts take the CUDA-core form, which converts an expert's
+// Whether up to 16 rows of a stack take the CUDA-core form, which converts an expert's
 // weights again for every row.  The other forms convert them once a holder: A = E (1 - (1 - 1/E)^T)
 // experts hold any of T rows routed alike.  In units of a weight's conversion on the CUDA cores the
 // mma.sync form takes 5/6 of one a weight and holder, the tcgen05 form (K too long for that one)
@@ -777,15 +777,15 @@ bool expert_rows_pay(const wq::ExpertArgs& a) {
   return (a.T - once * a.E * (1 - none)) * a.N * a.K <= ahead;
 }
 
-// Which form runs (all three where it says; microseconds, MXFP4 unless it says INT4).  One expert
-// that holds all rows is a plain product.
-//   CUDA cores: up to 16 rows over several experts by the rule above; the one or two rows of a
+// Which form runs (all three where it says; microseconds, MXFP4 unless it says INT4).  An MXFP4
+// stack of one expert is a plain product (the MXFP4 Linear's) and gives its bits.
+//   CUDA cores: up to 16 rows of a stack by the rule above; the one or two rows of a
 //     plain product while there are few weights to convert for each row (2^25), or where K is
 //     too long for the mma.sync form.
 //       plain, N x K of W            2048 x 2048   11008 x 2048   28672 x 4096   2048 x 11008
 //         1 row   cores / mma.sync    4.7 / 6.1     8.7 / 9.1      29 / 25        11.8 / (tcgen05) 13.6
 //         2 rows                      5.9 / 6.2    11.8 / 9.2      40 / 25        10.5 / 13.6
-//   mma.sync: at most 8 rows of a plain product; at most 5 min(E, T) rows over several experts (the
+//   mma.sync: at most 8 rows of one expert; at most 5 min(E, T) rows over several experts (the
 //     host does not know which of them hold rows), where the tcgen05 form has more items than one
 //     wave.  K up to 6656 (INT4 5888), whose rows fit shared memory: sharing a longer one in a
 //     cluster measured slower than the tcgen05 form (8 rows of 2051 x 11008: 16.7 / 14.9).
@@ -801,7 +801,8 @@ int launch_experts_fmt(const wq::ExpertArgs& a, const uint16_t* X, const void* p
   wq::ExpertArgs v = a;
   v.X = X; v.packed = static_cast<const uint8_t*>(packed);
   const bool serves = expert_gemv_serves<FMT>(a.K);
-  if (a.E > 1 ? expert_rows_pay<FMT>(a) : a.T <= 2 && (!serves || int64_t(a.T) * a.N * a.K <= 1 << 25))
+  const bool plain = FMT == wq::GEMM_MXFP4 && a.E == 1;
+  if (plain ? a.T <= 2 && (!serves || int64_t(a.T) * a.N * a.K <= 1 << 25) : expert_rows_pay<FMT>(a))
     return launch_expert_rows<FMT>(v, st);
   const bool few = a.E == 1 ? a.T <= wq::kVecRows
                             : a.T <= 5 * std::min(a.E, a.T) && expert_items(a) > wq::kTcMaxCtas;
